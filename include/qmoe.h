@@ -51,6 +51,7 @@ extern "C" {
 /* activation dtypes (hidden states, scales, output) */
 #define QMOE_DTYPE_F16 1
 #define QMOE_DTYPE_BF16 2
+#define QMOE_DTYPE_F32 3 /* rows of the sort by expert and of the MXFP4 operators only */
 
 /* gated activations on interleaved fc1 rows (row 2j = gate, 2j+1 = up)
  * [qmoe.rs, qmoe_activate with swiglu_fusion = 1; PR 32198, GeGLU uses the same
@@ -323,6 +324,126 @@ int qmoe_forward_ex(const void* hidden, const float* logits, int64_t T, int32_t 
                     int32_t dtype, void* out, int32_t* topk_ids_out, float* topk_w_out,
                     const qmoe_layer_opts* opts, void* workspace, size_t workspace_bytes,
                     void* stream);
+
+/*
+ * Tokens sorted by expert: the rows of all routes, expert by expert.
+ *   hidden          dtype [T, H], rows row_stride elements apart (row_stride
+ *                   >= H), aligned to its element; NULL together with rows:
+ *                   only the three maps are written
+ *   topk_ids        int32 [T, top_k]; a route whose id is outside [0, E) is
+ *                   dropped: it joins no expert
+ *   rows            dtype [T*top_k, H] out: row j is the token of route
+ *                   sorted_routes[j]; the rows of dropped routes, behind the
+ *                   last expert's, are zero
+ *   expert_offsets  int32 [E+1] out: expert e has the rows [offsets[e],
+ *                   offsets[e+1]); offsets[E] counts the kept routes
+ *   sorted_routes   int32 [T*top_k] out: the routes, experts ascending, routes
+ *                   ascending within an expert, the dropped ones last
+ *   route_rows      int32 [T, top_k] out: the row of each route, or -1 - row
+ *                   for a dropped one
+ *   workspace       >= qmoe_permute_workspace_size(T, top_k, E) bytes, 4-byte
+ *                   aligned; contents on entry do not matter (the size is 0
+ *                   for few routes, then workspace may be NULL)
+ * Requires 1 <= E <= 1024, 1 <= top_k <= 1024 (not bounded by E), T < 2^23,
+ * T*top_k < 2^31, 1 <= H <= 2^20; dtype F16, BF16 or F32.  T = 0 writes the
+ * offsets (all 0).  Rows are copied bit for bit.  The gradient with respect to
+ * hidden is qmoe_unpermute of the rows' gradient with weights NULL.
+ */
+size_t qmoe_permute_workspace_size(int64_t T, int32_t top_k, int32_t E);
+int qmoe_permute(const void* hidden, int64_t row_stride, int64_t T, int32_t H, int32_t dtype,
+                 const int32_t* topk_ids, int32_t top_k, int32_t E, void* rows,
+                 int32_t* expert_offsets, int32_t* sorted_routes, int32_t* route_rows,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows back to their tokens, with weights applied:
+ *   out[t] = sum over slots s, in slot order, of weights[t,s] * rows[route_rows[t,s]]
+ * in float32, rounded once.  Routes with route_rows outside [0, T*top_k)
+ * (dropped ones) add nothing, whatever their weight.
+ *   rows        dtype [T*top_k, H], rows row_stride elements apart
+ *   route_rows  int32 [T, top_k] as qmoe_permute writes it
+ *   weights     float32 [T, top_k], or NULL: every weight is 1
+ *   out         dtype [T, H] out; a token without kept routes gets zeros
+ * Sizes as qmoe_permute.  T = 0 returns QMOE_OK and enqueues nothing.
+ */
+int qmoe_unpermute(const void* rows, int64_t row_stride, const int32_t* route_rows,
+                   const float* weights, int64_t T, int32_t top_k, int32_t H, int32_t dtype,
+                   void* out, void* stream);
+
+/*
+ * The gradient of qmoe_unpermute.
+ *   grad_out      dtype [T, H], rows grad_stride elements apart
+ *   rows          as in qmoe_unpermute, or NULL together with grad_weights
+ *   weights       as in qmoe_unpermute
+ *   grad_rows     dtype [T*top_k, H] out: weights[t,s] * grad_out[t] at row
+ *                 route_rows[t,s], rounded once; zeros at the row of a dropped
+ *                 route
+ *   grad_weights  float32 [T, top_k] out (nullable): the dot product of
+ *                 grad_out[t] with the route's row, float32 sums in a fixed
+ *                 order; 0 for a dropped route
+ * Every row of grad_rows is written once when route_rows is qmoe_permute's (no
+ * row twice); rows that no entry of another table names are left as they were.
+ * grad_rows must not overlap grad_out or rows.
+ */
+int qmoe_unpermute_backward(const void* grad_out, int64_t grad_stride, const void* rows,
+                            int64_t row_stride, const int32_t* route_rows, const float* weights,
+                            int64_t T, int32_t top_k, int32_t H, int32_t dtype, void* grad_rows,
+                            float* grad_weights, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4, the Open Compute Project's MX
+ * formats): blocks of 32 consecutive values share one power-of-two scale.
+ *   codes   uint8 [..., K/2]: two e2m1 codes a byte, the lower index in the low
+ *           bits; code = sign << 3 | m with m = 0..7 for 0, 0.5, 1, 1.5, 2, 3,
+ *           4, 6.  16-byte aligned.
+ *   scales  uint8 [..., K/32]: 2^(byte - 127); 255 stands for NaN.
+ * K is a multiple of 32 (else QMOE_ERR_UNSUPPORTED).
+ *
+ * qmoe_mx_quantize: x dtype [rows, K], rows row_stride elements apart, to codes
+ * [rows, K/2] and scales [rows, K/32].  A block's scale exponent is
+ * floor(log2(max |x|)) - 2, at least -127; codes are x / scale rounded to
+ * nearest (ties to the even code), magnitudes above 6 to 6.  A zero block has
+ * the scale byte 0; a block with a NaN or an infinity has the scale byte 255
+ * and codes 0.  rows*K <= 2^34.
+ *
+ * qmoe_mx_quantize_columns: x dtype [E, rows, K] dense, blocks of 32 rows of
+ * one column (rows a multiple of 32, any K), to codes [E, K, rows/2] and scales
+ * [E, K, rows/32]: the transposed matrices, quantised along the axis that the
+ * gradient's product contracts.
+ *
+ * qmoe_mx_dequantize: the values, rounded once to dtype: out dtype [rows, K].
+ */
+int qmoe_mx_quantize(const void* x, int64_t row_stride, int64_t rows, int32_t K, int32_t dtype,
+                     uint8_t* codes, uint8_t* scales, void* stream);
+int qmoe_mx_quantize_columns(const void* x, int32_t E, int32_t rows, int32_t K, int32_t dtype,
+                             uint8_t* codes, uint8_t* scales, void* stream);
+int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K,
+                       int32_t dtype, void* out, void* stream);
+
+/*
+ * Grouped product of MXFP4 rows with MXFP4 expert weights:
+ *   out[r, n] = sum_k a[src(r), k] * w[e(r), n, k]
+ * accumulated in float32 by the scaled matrix instruction, rounded once.
+ *   a_codes, a_scales  [a_rows, K/2], [a_rows, K/32]
+ *   w_codes, w_scales  [E, N, K/2], [E, N, K/32]
+ *   expert_offsets     int32 [E+1], non-decreasing from 0: expert e(r) of the
+ *                      rows [offsets[e], offsets[e+1]) (clamped to [0, rows]);
+ *                      NULL only with E = 1: every row.  Rows from offsets[E]
+ *                      on are set to zero.
+ *   sorted_routes      NULL: src(r) = r (a_rows >= rows); or int32 [rows]:
+ *                      src(r) = sorted_routes[r] / top_k, so tokens quantised
+ *                      once serve all their routes; an entry that leads
+ *                      outside [0, a_rows) gives a row of zeros
+ *   top_k              >= 1, used with sorted_routes
+ *   out                dtype [rows, N] out (F16, BF16 or F32)
+ * Scales of 255 (NaN) make the outputs they enter NaN.  Requires 1 <= E <=
+ * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24.  rows = 0
+ * returns QMOE_OK and enqueues nothing.
+ */
+int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                   const uint8_t* w_codes, const uint8_t* w_scales, int32_t E, int32_t N,
+                   int32_t K, const int32_t* expert_offsets, const int32_t* sorted_routes,
+                   int32_t top_k, int64_t rows, int32_t dtype, void* out, void* stream);
 
 /*
  * Test hook: the dequantization of the weight-rounding kernels, written out

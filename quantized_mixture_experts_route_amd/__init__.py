@@ -27,6 +27,8 @@ ERR_WORKSPACE = -3
 ERR_HIP = -4
 DTYPE_F16 = 1
 DTYPE_BF16 = 2
+DTYPE_F32 = 3
+MX_BLOCK = 32
 ACT_SWIGLU = 0
 ACT_GEGLU = 1
 DECODE_MAX_ROUTES = 80
@@ -37,7 +39,9 @@ RAW_MULTI_BASE = 1
 EXPORTED = ("qmoe_last_error", "qmoe_route", "qmoe_router", "qmoe_worklist_capacity", "qmoe_group",
             "qmoe_workspace_size", "qmoe_forward", "qmoe_forward_ex", "qmoe_forward_noalloc",
             "qmoe_shared_workspace_size", "qmoe_forward_shared", "qmoe_dequantize",
-            "qmoe_raw_codes",
+            "qmoe_raw_codes", "qmoe_permute_workspace_size", "qmoe_permute", "qmoe_unpermute",
+            "qmoe_unpermute_backward", "qmoe_mx_quantize", "qmoe_mx_quantize_columns",
+            "qmoe_mx_dequantize", "qmoe_mx_matmul",
             "qmoe_timer_start", "qmoe_timer_stop")
 
 
@@ -103,12 +107,23 @@ def load_library(path: str = LIB_PATH):
                                         P, P, P, P, sz, P]
     lib.qmoe_dequantize.argtypes = [ctypes.POINTER(_Proj), i32, i32, i32, i32, f32, i32, P, P, P]
     lib.qmoe_raw_codes.argtypes = [ctypes.POINTER(_Proj), i32, i32, i32, i32, i32, P, P]
+    lib.qmoe_permute_workspace_size.argtypes = [i64, i32, i32]
+    lib.qmoe_permute_workspace_size.restype = sz
+    lib.qmoe_permute.argtypes = [P, i64, i64, i32, i32, P, i32, i32, P, P, P, P, P, sz, P]
+    lib.qmoe_unpermute.argtypes = [P, i64, P, P, i64, i32, i32, i32, P, P]
+    lib.qmoe_unpermute_backward.argtypes = [P, i64, P, i64, P, P, i64, i32, i32, i32, P, P, P]
+    lib.qmoe_mx_quantize.argtypes = [P, i64, i64, i32, i32, P, P, P]
+    lib.qmoe_mx_quantize_columns.argtypes = [P, i32, i32, i32, i32, P, P, P]
+    lib.qmoe_mx_dequantize.argtypes = [P, P, i64, i32, i32, P, P]
+    lib.qmoe_mx_matmul.argtypes = [P, P, i64, P, P, i32, i32, i32, P, P, i32, i64, i32, P, P]
     lib.qmoe_timer_start.argtypes = [i32]
     lib.qmoe_timer_stop.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
     for name in ("qmoe_route", "qmoe_router", "qmoe_group", "qmoe_forward", "qmoe_forward_ex",
                  "qmoe_forward_noalloc",
                  "qmoe_forward_shared",
-                 "qmoe_dequantize", "qmoe_raw_codes",
+                 "qmoe_dequantize", "qmoe_raw_codes", "qmoe_permute", "qmoe_unpermute",
+                 "qmoe_unpermute_backward", "qmoe_mx_quantize", "qmoe_mx_quantize_columns",
+                 "qmoe_mx_dequantize", "qmoe_mx_matmul",
                  "qmoe_timer_start", "qmoe_timer_stop"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -406,6 +421,273 @@ def raw_codes(proj: Projection, E: int, N: int, K: int, block_size: int, dtype: 
     _check(load_library().qmoe_raw_codes(ctypes.byref(p), E, N, K, dtype_code(dtype), variant,
                                          _ptr(q), _stream(stream)))
     return q
+
+
+# ------------------------------------------------ sorted by expert and back, MXFP4
+_ROW_DTYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _row_dtype(dt: torch.dtype, name: str) -> int:
+    code = _ROW_DTYPES.get(dt)
+    if code is None:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32, got {dt}")
+    return code
+
+
+def _tensor(t, name: str, device, dtype=None, shape=None) -> torch.Tensor:
+    """_dev for the operators below: also on `device` (that of the call's first tensor)."""
+    _dev(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _rows(t, name: str, device=None) -> int:
+    """Checks a matrix of rows (any row stride, neighbouring elements); its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    n, h = t.shape
+    if h < 1:
+        raise ValueError(f"{name} has no columns")
+    if h > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < h:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return t.stride(0) if n > 1 else h
+
+
+class _On:
+    """The device and the stream of a call: outputs are allocated for the stream that fills them,
+    and the launch goes to the tensors' device whichever is current."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.raw = self.stream.cuda_stream
+        # torch.cuda.stream() also makes the stream's device current
+        plain = stream is None and device.index == torch.cuda.current_device()
+        self._context = None if plain else torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._context is not None:
+            self._context.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._context is not None:
+            self._context.__exit__(*exc)
+        return False
+
+
+def permute_workspace_size(T: int, top_k: int, E: int) -> int:
+    return int(load_library().qmoe_permute_workspace_size(T, top_k, E))
+
+
+def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
+            workspace: Optional[torch.Tensor] = None, stream=None):
+    """Tokens sorted by expert: (rows [T*k, H], expert_offsets int32 [E+1], sorted_routes int32
+    [T*k], route_rows int32 [T, k]).
+
+    hidden: float16, bfloat16 or float32 [T, H], any row stride; None: rows is None and only the
+    maps are made.  Ids outside [0, E) drop their route: its row, behind the last expert's, is zero
+    and its route_rows entry is -1 - row."""
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be a tensor [T, top_k]")
+    dev = topk_ids.device
+    _dev(topk_ids, "topk_ids", torch.int32)
+    T, top_k = topk_ids.shape
+    stride, H, dt = 0, 0, DTYPE_F16
+    if hidden is not None:
+        stride, H, dt = _rows(hidden, "hidden", dev), hidden.shape[1], _row_dtype(hidden.dtype, "hidden")
+        if hidden.shape[0] != T:
+            raise ValueError(f"hidden has {hidden.shape[0]} rows, topk_ids {T}")
+    lib = load_library()
+    R = T * top_k
+    with _On(dev, stream) as on:
+        if workspace is None:
+            need = lib.qmoe_permute_workspace_size(T, top_k, E)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _tensor(workspace, "workspace", dev, torch.uint8)
+        rows = None if hidden is None else torch.empty((R, H), dtype=hidden.dtype, device=dev)
+        maps = torch.empty(max(E, 0) + 1 + 2 * R, dtype=torch.int32, device=dev)
+        offsets, order, route_rows = maps[:E + 1], maps[E + 1:E + 1 + R], maps[E + 1 + R:].view(T, top_k)
+        _check(lib.qmoe_permute(_ptr(hidden), stride, T, H, dt, _ptr(topk_ids), top_k, E, _ptr(rows),
+                                _ptr(offsets), _ptr(order), _ptr(route_rows), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(), on.raw))
+    return rows, offsets, order, route_rows
+
+
+def _back_sizes(route_rows):
+    if not isinstance(route_rows, torch.Tensor) or route_rows.dim() != 2:
+        raise ValueError("route_rows must be a tensor [T, top_k]")
+    _dev(route_rows, "route_rows", torch.int32)
+    return route_rows.device, route_rows.shape[0], route_rows.shape[1]
+
+
+def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows back to their tokens: out[t] = sum over slots of weights[t, s] * rows[route_rows[t, s]]
+    (float32 sums, rounded once; no weights: 1); dropped routes add nothing."""
+    dev, T, top_k = _back_sizes(route_rows)
+    stride, dt = _rows(rows, "rows", dev), _row_dtype(rows.dtype, "rows")
+    H = rows.shape[1]
+    if rows.shape[0] != T * top_k:
+        raise ValueError(f"rows has {rows.shape[0]} rows, expected {T * top_k}")
+    if weights is not None:
+        _tensor(weights, "weights", dev, torch.float32, (T, top_k))
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty((T, H), dtype=rows.dtype, device=dev)
+        else:
+            _tensor(out, "out", dev, rows.dtype, (T, H))
+        _check(load_library().qmoe_unpermute(_ptr(rows), stride, _ptr(route_rows), _ptr(weights), T, top_k,
+                                             H, dt, _ptr(out), on.raw))
+    return out
+
+
+def permute_backward(grad_rows: torch.Tensor, route_rows: torch.Tensor, *,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of permute with respect to hidden: the sum of a token's rows' gradients."""
+    return unpermute(grad_rows, route_rows, None, out=out, stream=stream)
+
+
+def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], route_rows: torch.Tensor,
+                       weights: Optional[torch.Tensor] = None, *, stream=None):
+    """The gradient of unpermute: (grad_rows [T*k, H], grad_weights float32 [T, k]).  rows None:
+    grad_weights is not computed (None), as for an unpermute without weights."""
+    dev, T, top_k = _back_sizes(route_rows)
+    gstride, dt = _rows(grad_out, "grad_out", dev), _row_dtype(grad_out.dtype, "grad_out")
+    H = grad_out.shape[1]
+    if grad_out.shape[0] != T:
+        raise ValueError(f"grad_out has {grad_out.shape[0]} rows, expected {T}")
+    stride = 0
+    if rows is not None:
+        stride = _rows(rows, "rows", dev)
+        if rows.dtype != grad_out.dtype or tuple(rows.shape) != (T * top_k, H):
+            raise ValueError(f"rows is {rows.dtype} {tuple(rows.shape)}, expected {grad_out.dtype} "
+                             f"{(T * top_k, H)}")
+    if weights is not None:
+        _tensor(weights, "weights", dev, torch.float32, (T, top_k))
+    with _On(dev, stream) as on:
+        grad_rows = torch.empty((T * top_k, H), dtype=grad_out.dtype, device=dev)
+        grad_weights = None
+        if rows is not None:
+            grad_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        _check(load_library().qmoe_unpermute_backward(
+            _ptr(grad_out), gstride, _ptr(rows), stride, _ptr(route_rows), _ptr(weights), T, top_k, H, dt,
+            _ptr(grad_rows), _ptr(grad_weights), on.raw))
+    return grad_rows, grad_weights
+
+
+def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
+    """MXFP4 codes (uint8 [..., K/2]) and scales (uint8 [..., K/32]) of x [..., K], blocks of 32 along
+    K (a matrix may have any row stride).  transpose: x [E, rows, K] or [rows, K] is quantised along
+    its rows, giving codes [E, K, rows/2] and scales [E, K, rows/32] of the transposed matrices."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA (HIP) tensor")
+    dt, dev = _row_dtype(x.dtype, "x"), x.device
+    if transpose:
+        if x.dim() not in (2, 3):
+            raise ValueError("x must have 2 or 3 dimensions to be quantised along its rows")
+        _dev(x, "x")
+        rows, K = x.shape[-2:]
+        E = x.shape[0] if x.dim() == 3 else 1
+        lead, width = (*x.shape[:-2], K), rows
+    else:
+        if x.dim() < 1:
+            raise ValueError("x must have at least 1 dimension")
+        K = x.shape[-1]
+        lead, width = x.shape[:-1], K
+        if x.dim() == 2:
+            rows, stride = x.shape[0], _rows(x, "x")
+        else:
+            _dev(x, "x")
+            rows, stride = math.prod(lead), K
+    with _On(dev, stream) as on:
+        codes = torch.empty((*lead, width // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((*lead, width // MX_BLOCK), dtype=torch.uint8, device=dev)
+        lib = load_library()
+        if transpose:
+            _check(lib.qmoe_mx_quantize_columns(_ptr(x), E, rows, K, dt, _ptr(codes), _ptr(scales), on.raw))
+        else:
+            _check(lib.qmoe_mx_quantize(_ptr(x), stride, rows, K, dt, _ptr(codes), _ptr(scales), on.raw))
+    return codes, scales
+
+
+def _mx(codes, scales, name: str, device):
+    """Checks a pair of codes [..., K/2] and scales [..., K/32]; returns K."""
+    _tensor(codes, f"{name}_codes", device, torch.uint8)
+    _tensor(scales, f"{name}_scales", device, torch.uint8)
+    if codes.dim() < 1 or scales.dim() != codes.dim() or codes.shape[:-1] != scales.shape[:-1]:
+        raise ValueError(f"{name}_codes {tuple(codes.shape)} and {name}_scales {tuple(scales.shape)} "
+                         "do not belong together")
+    K = codes.shape[-1] * 2
+    if K != scales.shape[-1] * MX_BLOCK:
+        raise ValueError(f"{name}_codes holds {K} values a row, {name}_scales {scales.shape[-1]} blocks "
+                         f"of {MX_BLOCK}")
+    return K
+
+
+def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype, *,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """What MXFP4 codes [..., K/2] with scales [..., K/32] stand for, [..., K] in dtype."""
+    dt = _row_dtype(dtype, "dtype")
+    _dev(codes, "codes")
+    dev = codes.device
+    K = _mx(codes, scales, "mx", dev)
+    shape = (*codes.shape[:-1], K)
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _tensor(out, "out", dev, dtype, shape)
+        _check(load_library().qmoe_mx_dequantize(_ptr(codes), _ptr(scales), math.prod(shape[:-1]), K, dt,
+                                                 _ptr(out), on.raw))
+    return out
+
+
+def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
+              w_scales: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None, *,
+              sorted_routes: Optional[torch.Tensor] = None, top_k: int = 1,
+              dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Grouped product of MXFP4 rows with MXFP4 expert weights: out [rows, N] in dtype.
+
+    a: [A, K] rows; w: [E, N, K] (or [N, K], one expert); expert_offsets int32 [E+1]: the rows of each
+    expert (may be omitted for one expert).  sorted_routes int32 [rows] (with top_k): row r takes
+    a's row sorted_routes[r] // top_k; without it row r takes a's row r.  Rows behind the last
+    expert's are zero."""
+    dt = _row_dtype(dtype, "dtype")
+    _dev(a_codes, "a_codes", torch.uint8)
+    dev = a_codes.device
+    K = _mx(a_codes, a_scales, "a", dev)
+    if _mx(w_codes, w_scales, "w", dev) != K:
+        raise ValueError(f"a has {K} values a row, w {w_codes.shape[-1] * 2}")
+    if a_codes.dim() != 2 or w_codes.dim() not in (2, 3):
+        raise ValueError("a must have 2 dimensions and w 2 or 3")
+    E, N = (1, w_codes.shape[0]) if w_codes.dim() == 2 else w_codes.shape[:2]
+    if expert_offsets is not None:
+        _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
+    rows = a_codes.shape[0]
+    if sorted_routes is not None:
+        _tensor(sorted_routes, "sorted_routes", dev, torch.int32)
+        if sorted_routes.dim() != 1:
+            raise ValueError("sorted_routes must have 1 dimension")
+        rows = sorted_routes.shape[0]
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty((rows, N), dtype=dtype, device=dev)
+        else:
+            _tensor(out, "out", dev, dtype, (rows, N))
+        _check(load_library().qmoe_mx_matmul(
+            _ptr(a_codes), _ptr(a_scales), a_codes.shape[0], _ptr(w_codes), _ptr(w_scales), E, N, K,
+            _ptr(expert_offsets), _ptr(sorted_routes), top_k, rows, dt, _ptr(out), on.raw))
+    return out
 
 
 def timer_start(stage: int):

@@ -13,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "expert_ops.h"
 #include "qmoe.h"
 #include "qmoe_internal.h"
 
@@ -63,6 +64,8 @@ int qmoe::set_error(int code, const char* fmt, ...)
     g_error = std::string("qmoe: ") + buf;
     return code;
 }
+
+void qmoe::clear_error() { g_error.clear(); }
 
 qmoe::LaunchEvents& qmoe::launch_events()
 {

@@ -1,0 +1,373 @@
+"""GPU tests of the MXFP4 operators: conversions bit for bit against a 64-bit definition, the grouped
+product against float64 sums of the values that codes and scales stand for."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_mixture_experts_route_amd as qm
+from tests import _expert_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def _exact(x):
+    return x.cpu().double().numpy()
+
+
+def _same(got, want):
+    return np.array_equal(got.cpu().numpy(), want)
+
+
+def _check_quantized(x):
+    codes, scales = qm.mx_quantize(x)
+    want_c, want_s = ref.quantize(_exact(x))
+    assert _same(scales, want_s)
+    assert _same(codes, ref.pack(want_c))
+    return codes, scales
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (17, 2048), (257, 160), (2, 14336)])
+def test_quantize(rows, K, dtype):
+    g = torch.Generator().manual_seed(rows * K)
+    x = torch.randn(rows, K, generator=g) * torch.exp2(torch.randint(-12, 12, (rows, 1), generator=g))
+    _check_quantized(x.to(dtype).cuda())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_quantize_borders_and_neighbours(dtype):
+    # every border between neighbouring e2m1 values, the values themselves and the type's next
+    # values on both sides, at many scales (a 4 in the block fixes its scale)
+    points = np.array([0, 0.25, 0.5, 0.75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7, 7.9])
+    t = torch.tensor(points, dtype=torch.float32).to(dtype)
+    up = torch.nextafter(t.float(), torch.tensor(100.0)) if dtype == F32 else (t.view(torch.int16) + 1).view(dtype)
+    dn = torch.nextafter(t.float(), torch.tensor(0.0)) if dtype == F32 else (t.view(torch.int16) - 1).clamp(min=0).view(dtype)
+    v = torch.cat([t, up.to(dtype), dn.to(dtype)])
+    v = torch.cat([v, -v])
+    v = torch.cat([v, torch.zeros(-v.numel() % 31, dtype=dtype)]).reshape(-1, 31)
+    block = torch.cat([v, torch.full((v.shape[0], 1), 4.0, dtype=dtype)], 1)
+    for e in (range(-10, 13) if dtype == F16 else range(-120, 121, 3)):
+        x = (block.double() * 2.0 ** e).to(dtype)
+        _check_quantized(x.cuda())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_quantize_every_pattern(dtype):
+    # all 65,536 patterns of the type, each as its block's largest and beside a fixed companion
+    bits = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16)
+    x = bits.view(dtype).reshape(-1, 1).repeat(1, 32)
+    x[:, 1::2] = 0
+    x[:, 2::8] = -x[:, 2::8]
+    _check_quantized(x.cuda())
+    y = bits.view(dtype).reshape(-1, 32)  # 32 neighbouring patterns a block
+    _check_quantized(y.cuda())
+
+
+def test_quantize_float32_extremes():
+    tiny = 2.0 ** -149
+    rows = [[0.0] * 32, [-0.0] * 32, [tiny] + [0.0] * 31, [2.0 ** -126, -tiny] * 16,
+            [2.0 ** -125, 2.0 ** -128, -2.0 ** -127] + [2.0 ** -126 * 1.5] * 29,
+            [2.0 ** -124, 2.0 ** -129] * 16, [3.4028234663852886e38, -1e38] * 16,
+            [1e38] * 31 + [float("inf")], [1.0] * 31 + [float("nan")], [-float("inf")] + [0.0] * 31,
+            [2.0 ** 127] + [2.0 ** 100] * 31]
+    x = torch.tensor(rows, dtype=torch.float64).to(F32)
+    codes, scales = _check_quantized(x.cuda())
+    assert scales.reshape(-1).tolist()[7:10] == [255, 255, 255]
+    assert scales[0].item() == 0 and codes[0].eq(0).all() and codes[1].eq(0x88).all()
+
+
+def test_quantize_row_stride_and_leading_dimensions():
+    wide = torch.randn(37, 300, device="cuda").to(BF16)
+    _check_quantized(wide[:, 7:7 + 96])
+    _check_quantized(torch.randn(3, 5, 64, device="cuda"))
+    _check_quantized(torch.randn(64, device="cuda").to(F16))
+    assert qm.mx_quantize(torch.empty(0, 64, device="cuda"))[0].shape == (0, 32)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("E,rows,K", [(1, 32, 1), (2, 64, 37), (3, 320, 130), (1, 1056, 65), (2, 256, 128),
+                                      (1, 32, 2047), (5, 96, 64)])
+def test_quantize_columns(E, rows, K, dtype):
+    g = torch.Generator().manual_seed(rows + K)
+    x = (torch.randn(E, rows, K, generator=g) * torch.exp2(torch.randint(-9, 9, (E, 1, K), generator=g))).to(dtype)
+    x[0, 5, 0] = float("nan")
+    codes, scales = qm.mx_quantize(x.cuda(), transpose=True)
+    want_c, want_s = ref.quantize(_exact(x.transpose(1, 2).contiguous()))
+    assert _same(scales, want_s) and _same(codes, ref.pack(want_c))
+    c2, s2 = qm.mx_quantize(x[0].cuda(), transpose=True)
+    assert torch.equal(c2, codes[0]) and torch.equal(s2, scales[0])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_dequantize_every_code_and_scale(dtype):
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(256, 1)  # 16 blocks of 32 a row
+    scales = torch.arange(256, dtype=torch.int32).to(torch.uint8).reshape(256, 1).repeat(1, 16)
+    got = qm.mx_dequantize(codes.cuda(), scales.cuda(), dtype).cpu()
+    # e2m1 values times powers of two are exact in float64 and in float32 down to its subnormals;
+    # above its range they are infinite
+    want = torch.from_numpy(ref.values(codes.numpy(), scales.numpy())).to(F32).to(dtype)
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan])
+
+
+def test_quantize_dequantize_is_a_projection():
+    x = torch.randn(64, 512, device="cuda")
+    c, s = qm.mx_quantize(x)
+    y = qm.mx_dequantize(c, s, F32)
+    c2, s2 = qm.mx_quantize(y)
+    # values of the format that reach 4 in their block come back as they are
+    top = y.reshape(64, 16, 32).abs().amax(-1)
+    assert torch.equal(qm.mx_dequantize(c2, s2, F32), y) and int((top > 0).sum()) == top.numel()
+    # |error| <= half the widest gap (1 of 4..6, scale units), or the saturation above 6 (below 2)
+    scale = torch.exp2(s.float() - 127).repeat_interleave(32, -1)
+    assert bool(((y - x).abs() <= 2 * scale).all())
+
+
+def _operand(rng, shape, lo=112, hi=128):
+    codes = rng.integers(0, 256, (*shape[:-1], shape[-1] // 2), dtype=np.uint8)
+    scales = rng.integers(lo, hi, (*shape[:-1], shape[-1] // 32), dtype=np.uint8)
+    return codes, scales
+
+
+def _matmul_case(T, k, E, K, N, dtype, gather, seed, dropped=0.0, counts=None, lo=112, hi=128):
+    """Runs one product and compares every output; returns it."""
+    rng = np.random.default_rng(seed)
+    R = T * k
+    if counts is None:
+        ids = rng.integers(0, E, (T, k)).astype(np.int32)
+        ids[rng.random((T, k)) < dropped] = -1
+    else:
+        ids = np.repeat(np.arange(len(counts)), counts).astype(np.int32).reshape(T, k)
+        ids[ids >= E] = -1
+    offsets, order, _ = ref.sort(ids, E)
+    ac, as_ = _operand(rng, (T if gather else R, K), lo, hi)
+    wc, ws = _operand(rng, (E, N, K), lo, hi)
+    dev = [torch.from_numpy(v).cuda() for v in (ac, as_, wc, ws, offsets.astype(np.int32), order.astype(np.int32))]
+    out = qm.mx_matmul(*dev[:5], sorted_routes=dev[5] if gather else None, top_k=k, dtype=dtype)
+    assert out.dtype == dtype and tuple(out.shape) == (R, N)
+    a = ref.values(ac, as_)
+    a = a[order // k] if gather else a
+    want, mag = np.zeros((R, N)), np.zeros((R, N))
+    for e in range(E):
+        if offsets[e + 1] > offsets[e]:
+            sl = slice(offsets[e], offsets[e + 1])
+            w = ref.values(wc[e], ws[e])
+            want[sl], mag[sl] = a[sl] @ w.T, np.abs(a[sl]) @ np.abs(w.T)
+    got = out.double().cpu().numpy()
+    # every product is exact in float32; K roundings (or truncations: a whole unit, 2 U32) of partial
+    # sums no larger than mag, then one rounding to the type
+    # float32 values below 2^-126 may count as zero: K terms of that size at most
+    acc = K * 2 * ref.U32 * mag + K * 2.0 ** -126
+    tol = acc + ref.HALF_STEP[dtype] * (np.abs(want) + acc) + ref.HALF_MIN[dtype]
+    inside = (np.abs(want) + tol < torch.finfo(dtype).max) & (mag < torch.finfo(F32).max)
+    assert inside.mean() > 0.9
+    assert np.all(np.abs(got - want)[inside] <= tol[inside])
+    assert np.all(got[offsets[E]:] == 0)
+    return out
+
+
+# T, k, E, K, N, dtype, gather, dropped
+PRODUCT = [
+    (1, 1, 1, 32, 1, F32, False, 0.0),       # the smallest of everything
+    (1, 2, 8, 2048, 512, F16, True, 0.0),    # one token
+    (1, 8, 40, 512, 96, BF16, True, 0.0),
+    (6, 10, 64, 256, 200, BF16, True, 0.0),
+    (5, 3, 4, 96, 33, F32, True, 0.3),       # K of three blocks, odd N, dropped routes
+    (17, 2, 3, 160, 127, F16, False, 0.2),
+    (40, 2, 8, 544, 130, BF16, True, 0.0),
+    (100, 1, 1, 1024, 256, F32, False, 0.0),
+    (130, 3, 5, 768, 257, BF16, True, 0.1),
+    (256, 2, 2, 320, 300, F16, True, 0.0),
+    (300, 4, 6, 1056, 520, BF16, True, 0.05),
+    (512, 1, 700, 64, 40, F32, True, 0.1),   # more experts than rows a tile
+    (700, 2, 2, 256, 513, F32, False, 0.0),
+    (1000, 2, 3, 2080, 264, BF16, True, 0.0),
+    (1500, 1, 1, 512, 640, F16, False, 0.0),
+    (9, 1, 2, 64, 5000, BF16, False, 0.5),
+]
+
+
+@pytest.mark.parametrize("T,k,E,K,N,dtype,gather,dropped", PRODUCT)
+def test_matmul(T, k, E, K, N, dtype, gather, dropped):
+    _matmul_case(T, k, E, K, N, dtype, gather, T + K + N, dropped)
+
+
+@pytest.mark.parametrize("counts", [
+    [0, 0, 0, 31, 1], [32, 0, 0, 0], [1, 0, 33, 0, 30], [64, 63, 65], [0, 0, 128], [127, 129],
+    [1] * 16, [0] * 9 + [16] + [0] * 6, [255, 1, 257, 0, 511], [17, 15, 0, 48, 16],
+])
+def test_matmul_row_counts(counts):
+    # experts without rows, rows around the tile borders
+    _matmul_case(sum(counts), 1, len(counts), 288, 144, F32, False, 1 + len(counts), counts=counts)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+@pytest.mark.parametrize("K", [32, 1024, 1312])
+def test_matmul_dense_row_counts(rows, K):
+    _matmul_case(rows, 1, 1, K, 272, BF16, False, rows + K)
+
+
+def test_matmul_scale_range():
+    # products of scales far from 1: 2^-120 .. 2^120 in float32
+    for lo, hi in ((60, 80), (172, 184), (0, 120), (100, 155)):
+        _matmul_case(33, 2, 4, 256, 96, F32, True, lo + hi, lo=lo, hi=hi)
+
+
+def _small(rows=5, K=64, N=40, E=2):
+    rng = np.random.default_rng(0)
+    ac, as_ = _operand(rng, (rows, K))
+    wc, ws = _operand(rng, (E, N, K))
+    return [torch.from_numpy(v).cuda() for v in (ac, as_, wc, ws)]
+
+
+@pytest.mark.parametrize("rows", [5, 100, 400])
+def test_matmul_nan_scales_stay_in_their_row_and_column(rows):
+    a, sa, w, sw = _small(rows=rows, N=300)
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+    clean = qm.mx_matmul(a, sa, w, sw, off, dtype=F32)
+    sa[1, 1] = 255
+    sw[1, 7, 0] = 255
+    out = qm.mx_matmul(a, sa, w, sw, off, dtype=F32)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[1] = True
+    bad[rows // 2:, 7] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("rows", [7, 90, 300])
+def test_matmul_bad_tables_stay_inside(rows):
+    # routes that lead outside the rows of a give zero rows; offsets outside [0, rows] are clamped
+    a, sa, w, sw = _small(rows=rows, N=72)
+    off = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+    good = qm.mx_matmul(a, sa, w, sw, off, dtype=F32)
+    routes = torch.arange(rows, dtype=torch.int32, device="cuda") * 3
+    want = good.clone()
+    for at, bad in ((0, -1), (1, -2 ** 31), (rows - 2, 2 ** 31 - 1), (rows - 1, 3 * rows)):
+        routes[at] = bad
+        want[at] = 0
+    got = qm.mx_matmul(a, sa, w, sw, off, sorted_routes=routes, top_k=3, dtype=F32)
+    assert torch.equal(got, want)
+    off = torch.tensor([-2 ** 31, rows // 3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    assert torch.equal(qm.mx_matmul(a, sa, w, sw, off, dtype=F32), good)
+
+
+def test_matmul_into_a_given_output_and_its_neighbours():
+    a, sa, w, sw = _small(rows=37, N=45)
+    off = torch.tensor([0, 20, 30], dtype=torch.int32, device="cuda")
+    buf = torch.full((39, 45), 7.0, device="cuda")
+    qm.mx_matmul(a, sa, w, sw, off, dtype=F32, out=buf[1:38])
+    assert torch.equal(buf[1:38], qm.mx_matmul(a, sa, w, sw, off, dtype=F32))
+    assert buf[0].eq(7).all() and buf[38].eq(7).all() and buf[31:38].eq(0).all()
+
+
+def test_matmul_repeats_bit_for_bit():
+    for T, E in ((4, 8), (300, 3)):
+        first = _matmul_case(T, 2, E, 1024, 520, F32, True, 9)
+        for _ in range(2):
+            assert torch.equal(first, _matmul_case(T, 2, E, 1024, 520, F32, True, 9))
+
+
+def test_matmul_weights_past_32_bits():
+    # the last expert's codes lie past 2^32 bytes: 260 experts of 8192 x 4096 (4.4 GB of codes)
+    E, N, K = 260, 8192, 4096
+    wc = torch.zeros((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    ws = torch.full((E, N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    wc[-1] = torch.randint(0, 256, (N, K // 2), device="cuda").to(torch.uint8)
+    for rows in (2, 40):
+        a = torch.randint(0, 256, (rows, K // 2), device="cuda").to(torch.uint8)
+        sa = torch.full((rows, K // 32), 127, dtype=torch.uint8, device="cuda")
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[-1] = rows
+        out = qm.mx_matmul(a, sa, wc, ws, off, dtype=F32)
+        alone = qm.mx_matmul(a, sa, wc[-1].contiguous(), ws[-1].contiguous(), dtype=F32)
+        want = qm.mx_dequantize(a, sa, F32).double() @ qm.mx_dequantize(wc[-1], ws[-1], F32).double().T.contiguous()
+        mag = qm.mx_dequantize(a, sa, F32).abs().double() @ qm.mx_dequantize(wc[-1], ws[-1], F32).abs().double().T.contiguous()
+        assert bool(((out.double() - want).abs() <= (K * 2 + 1) * ref.U32 * mag).all())
+        assert torch.equal(out, alone)
+
+
+def _swiglu(y):
+    g, u = y[:, 0::2].float(), y[:, 1::2].float()
+    return g * torch.sigmoid(g) * u
+
+
+def _mx_layer(x, ids, wts, w1, w2, E, k):
+    """Sorted, both projections on MXFP4 operands, brought back with the routing weights."""
+    _, offsets, order, rr = qm.permute(None, ids, E)
+    y = qm.mx_matmul(*qm.mx_quantize(x), *w1, offsets, sorted_routes=order, top_k=k, dtype=F32)
+    act = _swiglu(y)
+    rows = qm.mx_matmul(*qm.mx_quantize(act), *w2, offsets, dtype=x.dtype)
+    return offsets, order, rr, y, act, rows, qm.unpermute(rows, rr, wts)
+
+
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_layer_of_the_operators_and_its_gradient(T):
+    # route -> sort -> quantise -> product -> SwiGLU -> quantise -> product -> back, and the gradient
+    # with respect to the product's rows and the routing weights, each step against float64 on the
+    # values the step before really gave
+    H, I, E, k, dtype = 128, 192, 6, 2, BF16
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    m1 = torch.randn(E, 2 * I, H, generator=g, device="cuda") * H ** -0.5
+    m2 = torch.randn(E, H, I, generator=g, device="cuda") * I ** -0.5
+    ids, wts = qm.route(torch.randn(T, E, generator=g, device="cuda"), k)
+    w1, w2 = qm.mx_quantize(m1), qm.mx_quantize(m2)
+    offsets, order, rr, y, act, rows, out = _mx_layer(x, ids, wts, w1, w2, E, k)
+    o = offsets.tolist()
+
+    def check(got, a, w, dt):
+        a, w = a.double(), qm.mx_dequantize(*w, F32).double()
+        for e in range(E):
+            s = slice(o[e], o[e + 1])
+            want, mag = a[s] @ w[e].T.contiguous(), a[s].abs() @ w[e].abs().T.contiguous()
+            tol = (2 * a.shape[1] * ref.U32 + ref.HALF_STEP[dt]) * mag * 1.01
+            assert bool(((got[s].double() - want).abs() <= tol).all())
+
+    xq = qm.mx_dequantize(*qm.mx_quantize(x), F32)
+    check(y, xq[order.long() // k], w1, F32)
+    check(rows, qm.mx_dequantize(*qm.mx_quantize(act), F32), w2, dtype)
+    want, mag = ref.unpermute(rows.double().cpu().numpy(), rr.cpu().numpy(), wts.double().cpu().numpy())
+    tol = k * ref.U32 * mag + ref.HALF_STEP[dtype] * mag * 1.01
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tol)
+
+    # gradient: back through the weighted sum, then the product's gradient on fc2 quantised along
+    # its other axis
+    grad = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    grad_rows, grad_w = qm.unpermute_backward(grad, rows, rr, wts)
+    m2t = qm.mx_quantize(m2, transpose=True)
+    assert tuple(m2t[0].shape) == (E, I, H // 2)
+    grad_act = qm.mx_matmul(*qm.mx_quantize(grad_rows), *m2t, offsets, dtype=F32)
+    check(grad_act, qm.mx_dequantize(*qm.mx_quantize(grad_rows), F32), m2t, F32)
+    want_w = (grad.double()[:, None] * rows.double()[rr.long()]).sum(-1)
+    mag_w = (grad.double()[:, None] * rows.double()[rr.long()]).abs().sum(-1)
+    assert bool(((grad_w.double() - want_w).abs() <= (H + 1) * ref.U32 * mag_w).all())
+
+
+def test_layer_of_the_operators_captured():
+    T, H, I, E, k = 24, 256, 128, 8, 2
+    x = torch.randn(T, H, device="cuda").to(F16)
+    logits = torch.randn(T, E, device="cuda")
+    w1 = qm.mx_quantize(torch.randn(E, 2 * I, H, device="cuda") * H ** -0.5)
+    w2 = qm.mx_quantize(torch.randn(E, H, I, device="cuda") * I ** -0.5)
+
+    def step():
+        ids, wts = qm.route(logits, k)
+        return _mx_layer(x, ids, wts, w1, w2, E, k)[-1]
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(4):
+        x.copy_(torch.randn(T, H, device="cuda").to(F16))
+        logits.copy_(torch.randn(T, E, device="cuda"))
+        want = step().clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured, want)
