@@ -17,6 +17,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int kMaxExperts = 1024;
 constexpr int kE2M1 = 4;  // operand format code of the scaled matrix instructions
 
 __device__ inline i32x8 operand(u32x4 v)
@@ -103,10 +104,409 @@ __global__ __launch_bounds__(256) void product_kernel(MxMatmulArgs a)
     }
 }
 
+// ---------------------------------------------------------------- tiled kernel
+// A workgroup of WM x WN wavefronts computes BM = 32 MT WM rows against
+// BN = 32 NT WN weight rows; a wavefront MT x NT blocks of 32 x 32.  W is the
+// instruction's first operand, so a lane's registers run along n and its
+// results leave as 16-byte stores.
+//
+// K runs in steps of 128 values: 64 bytes of codes a row, written to LDS by
+// the load itself (buffer_load ... lds) into one of kStages stages, three
+// steps ahead.  A group of four steps needs 16 bytes of scales a row, loaded
+// one group ahead into one of two buffers; a lane reads the 16 bytes once a
+// group and picks its byte by shift and operand select.  One barrier a step:
+// it tells that the step's stage has landed and that the stage read before is
+// free.  Loads run on over the end of a tile into the workgroup's next one, so
+// only its first tile waits for memory.
+//
+// LDS rows are 64 bytes (16 banks); the 16-byte chunk of row r sits in slot
+// chunk ^ (r / 4 % 4), so that 16 rows read at one chunk cover all 64 banks.
+//
+// WHOLE: K is a multiple of 512 and the scale rows are 16-byte aligned, so
+// scales take the direct path to LDS too and no step has a tail.  Otherwise
+// scales go through registers, byte by byte at the end of a row, and codes
+// behind the row's end are read out of the buffer's bounds, which gives 0.
+constexpr int kStages = 4;
+constexpr int kStepBytes = 64;   // codes of one row and step
+constexpr int kGroupSteps = 4;   // steps whose scales are loaded together: 16 bytes a row
+constexpr uint32_t kOutside = 0x80000000u;  // a byte offset behind every buffer
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+
+// 16 bytes a lane from the buffer to LDS at `to` + 16 * lane (to is uniform).
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset, void* to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, lane_offset,
+                                             offset, 0, 0);
+}
+
+template <int DT>
+__device__ inline uint32_t pack_pair(float lo, float hi)
+{
+    if constexpr (DT == kBF16) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+    } else {
+        return pack2(Dt<kF16>::from_float(lo), Dt<kF16>::from_float(hi));
+    }
+}
+
+// A lane's 16 results of one block: columns n + 8 q + 4 half + (0..3) of its row.
+template <int DT>
+__device__ inline void store_block(typename RowType<DT>::Raw* out, int n, int N, int half, const f32x16& acc, bool zero)
+{
+    typedef typename RowType<DT>::Raw Raw;
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int at = n + 8 * q + 4 * half;
+            RowVec<float, 4> v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.v[i] = zero ? 0.0f : acc[4 * q + i];
+            if (at + 4 <= N) {
+                store_vec<float, 4>(out + at, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (at + i < N) out[at + i] = v.v[i];
+                }
+            }
+        }
+    } else {
+        // the halves trade four columns, so that each lane holds eight neighbours
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const auto sw = __builtin_amdgcn_permlane32_swap(
+                    pack_pair<DT>(acc[4 * q + 2 * i], acc[4 * q + 2 * i + 1]),
+                    pack_pair<DT>(acc[4 * q + 4 + 2 * i], acc[4 * q + 5 + 2 * i]), false, false);
+                v[i] = zero ? 0u : sw[0];
+                v[2 + i] = zero ? 0u : sw[1];
+            }
+            const int at = n + 8 * q + 8 * half;
+            RowVec<Raw, 8> y;
+            __builtin_memcpy(&y, v, 16);
+            if (at + 8 <= N) {
+                store_vec<Raw, 8>(out + at, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (at + i < N) out[at + i] = y.v[i];
+                }
+            }
+        }
+    }
+}
+
+// m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
+template <int BM>
+__device__ void build_tile_list(int* first, const int32_t* offsets, int E, int rows)
+{
+    if (threadIdx.x < kWave) {
+        int carry = 0;
+        for (int base = 0; base < E; base += kWave) {
+            const int e = base + (int)threadIdx.x;
+            int tiles = 0;
+            if (e < E) {
+                const int lo = offsets ? min(max(offsets[e], 0), rows) : 0;
+                const int hi = offsets ? min(max(offsets[e + 1], lo), rows) : rows;
+                tiles = (hi - lo + BM - 1) / BM;
+            }
+            int incl = tiles;
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int y = __shfl_up(incl, d, kWave);
+                if ((int)threadIdx.x >= d) incl += y;
+            }
+            if (e < E) first[e] = carry + incl - tiles;
+            carry += __shfl(incl, kWave - 1, kWave);
+        }
+        if (threadIdx.x == 0) first[E] = carry;
+    }
+    __syncthreads();
+}
+
+struct TileItem {
+    int expert;
+    int row0;
+    int n;   // rows; 0: no item
+    int n0;  // first column
+};
+
+template <int BM, int BN>
+__device__ TileItem item_at(const int* first, const int32_t* offsets, int E, int rows, int n_tiles, int item,
+                            int end)
+{
+    if (item >= end) return TileItem{0, 0, 0, 0};
+    int lo = 0, hi = E - 1;  // the last expert whose first item is <= item
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] * n_tiles <= item) lo = mid; else hi = mid - 1;
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    const int base = __builtin_amdgcn_readfirstlane(first[lo]);
+    const int m_tiles = __builtin_amdgcn_readfirstlane(first[lo + 1]) - base;
+    const int local = item - base * n_tiles;
+    const int nt = local / m_tiles;  // neighbouring items share the weights
+    const int r_lo = offsets ? min(max(offsets[lo], 0), rows) : 0;
+    const int r_hi = offsets ? min(max(offsets[lo + 1], r_lo), rows) : rows;
+    const int row0 = r_lo + (local - nt * m_tiles) * BM;
+    return TileItem{lo, row0, min(BM, r_hi - row0), nt * BN};
+}
+
+template <int DT, int MT, int NT, int WM, int WN, bool WHOLE>
+__global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
+{
+    typedef typename RowType<DT>::Raw Raw;
+    constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN, ROWS = BM + BN;
+    constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    constexpr int LOADS = ROWS / 16 / WAVES;    // code loads of a wavefront and step: 16 rows each
+    constexpr int LOADS_A = BM / 16 / WAVES;
+    constexpr int SCALE_LOADS = (ROWS / 64 + WAVES - 1) / WAVES;  // scale loads: 64 rows each
+    static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0 && BM % 64 == 0 && BN % 64 == 0, "load split");
+
+    // one array for all of it: between arrays of their own the compiler tells apart what a load to
+    // LDS writes and waits for every such load before it reads LDS
+    constexpr int STAGE = ROWS * kStepBytes, SCALES = kStages * STAGE, LIST = SCALES + 2 * ROWS * 16;
+    __shared__ __align__(16) uint8_t lds[LIST + (kMaxExperts + 1) * 4];
+    uint8_t* const scales = lds + SCALES;
+    int* const first = reinterpret_cast<int*>(lds + LIST);
+
+    const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int K2 = a.K / 2, blocks = a.K / 32;
+    const int groups = (a.K + 128 * kGroupSteps - 1) / (128 * kGroupSteps);
+
+    build_tile_list<BM>(first, a.offsets, a.E, a.rows);
+    const int n_tiles = (a.N + BN - 1) / BN;
+    const int total = first[a.E] * n_tiles;
+    // workgroups go to the 8 dies in turn: each die takes one run of items, so
+    // that the workgroups of a die share rows and weights in its L2
+    const int per_die = gridDim.x / 8;
+    const int die = blockIdx.x % 8;
+    const int end = (int)((int64_t)total * (die + 1) / 8);
+    int next_item = (int)((int64_t)total * die / 8) + blockIdx.x / 8;
+
+    // rows behind the last expert's are zero
+    if (a.offsets) {
+        const int64_t lo = (int64_t)min(max(a.offsets[a.E], 0), a.rows) * a.N, hi = (int64_t)a.rows * a.N;
+        for (int64_t i = lo + blockIdx.x * THREADS + threadIdx.x; i < hi; i += (int64_t)gridDim.x * THREADS) {
+            ((Raw*)a.out)[i] = RowType<DT>::round(0.0f);
+        }
+    }
+
+    // ---- the loading side: an item and a group, up to four steps ahead
+    TileItem load_tile;
+    int load_group = 0;
+    uint32_t code_at[LOADS];        // byte offset of the lane's chunk at step 0
+    uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's scale row
+    __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
+    const uint8_t* w_scale_base = nullptr;
+
+    auto a_row = [&](const TileItem& t, int r) -> int {  // source row of product row r, clamped into a
+        const int row = t.row0 + min(r, t.n - 1);
+        if (!a.sorted_routes) return row;
+        const int route = a.sorted_routes[row];
+        const int src = route / a.top_k;
+        return route < 0 || src >= a.a_rows ? 0 : src;
+    };
+    auto start_item = [&]() {
+        load_tile = item_at<BM, BN>(first, a.offsets, a.E, a.rows, n_tiles, next_item, end);
+        next_item += per_die;
+        load_group = 0;
+        const TileItem& t = load_tile;
+        const bool on = t.n > 0;
+        const int w_rows = on ? min(BN, a.N - t.n0) : 0;
+        const int64_t w0 = (int64_t)t.expert * a.N + t.n0;
+        a_buf = buffer_of(a.a_codes, on ? (uint32_t)(a.a_rows * K2) : 0u);
+        w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
+        as_buf = buffer_of(a.a_scales, on ? (uint32_t)(a.a_rows * blocks) : 0u);
+        ws_buf = buffer_of(a.w_scales + w0 * blocks, (uint32_t)(w_rows * blocks));
+        w_scale_base = a.w_scales + w0 * blocks;
+        const uint32_t chunk = (uint32_t)((lane & 3) ^ (lane >> 4)) * 16;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int r = (j * WAVES + wave) * 16 + (lane >> 2);
+            uint32_t row = 0;
+            if (on) row = j < LOADS_A ? a_row(t, r) : min(r - BM, w_rows - 1);
+            code_at[j] = row * K2 + chunk;
+        }
+#pragma unroll
+        for (int j = 0; j < SCALE_LOADS; ++j) {
+            const int r = (j * WAVES + wave) * 64 + lane;
+            uint32_t row = 0;
+            if (on && r < ROWS) row = r < BM ? a_row(t, r) : min(r - BM, w_rows - 1);
+            scale_at[j] = row * blocks;
+        }
+    };
+    // codes of step s of the loading side's group into stage s
+    auto load_codes = [&](int s) {
+        const uint32_t at = (uint32_t)(load_group * kGroupSteps + s) * kStepBytes;
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            uint32_t off = code_at[j];
+            if constexpr (!WHOLE) {
+                const uint32_t chunk = (uint32_t)((lane & 3) ^ (lane >> 4)) * 16;
+                if (at + chunk >= (uint32_t)K2) off = kOutside;
+            }
+            load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + s * STAGE + (j * WAVES + wave) * 16 * kStepBytes);
+        }
+    };
+    u32x4 scale_regs[WHOLE ? 1 : SCALE_LOADS];
+    auto load_scales = [&](int buffer) {
+#pragma unroll
+        for (int j = 0; j < SCALE_LOADS; ++j) {
+            const int r0 = (j * WAVES + wave) * 64;
+            if (r0 >= ROWS) continue;
+            if constexpr (WHOLE) {
+                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], load_group * 16, scales + (buffer * ROWS + r0) * 16);
+            } else {
+                u32x4 v = {};
+                if (load_tile.n > 0) {
+                    const uint8_t* p = (r0 < BM ? a.a_scales : w_scale_base) + scale_at[j] + load_group * 16;
+                    const int left = blocks - load_group * 16;
+                    if (left >= 16) {
+                        __builtin_memcpy(&v, p, 16);
+                    } else {
+                        uint64_t part[2] = {};
+#pragma unroll 1
+                        for (int i = 0; i < left; ++i) {
+                            const uint64_t b = (uint64_t)p[i] << (8 * (i & 7));
+                            if (i < 8) part[0] |= b; else part[1] |= b;
+                        }
+                        __builtin_memcpy(&v, part, 16);
+                    }
+                }
+                scale_regs[j] = v;
+            }
+        }
+    };
+    auto store_scales = [&](int buffer) {  // the register path's second half
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (int j = 0; j < SCALE_LOADS; ++j) {
+                const int r0 = (j * WAVES + wave) * 64;
+                if (r0 < ROWS) *reinterpret_cast<u32x4*>(scales + (buffer * ROWS + r0 + lane) * 16) = scale_regs[j];
+            }
+        }
+    };
+
+    start_item();
+    load_scales(0);
+    store_scales(0);
+    load_codes(0);
+    load_codes(1);
+    load_codes(2);
+
+    const uint32_t swizzle = (c >> 2) & 3;
+    const uint32_t read_at[2] = {c * 64u + ((half ^ swizzle) * 16), c * 64u + (((2 + half) ^ swizzle) * 16)};
+    int buffer = 0;
+    while (load_tile.n > 0) {
+        const TileItem tile = load_tile;
+        f32x16 acc[NT][MT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
+        }
+        for (int g = 0; g < groups; ++g) {
+            u32x4 sw[NT], sa[MT];
+#pragma unroll
+            for (int s = 0; s < kGroupSteps; ++s) {
+                // step s has landed once only the loads of the two steps behind it are left
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LOADS) : "memory");
+                if (s == 0) {
+                    load_codes(3);
+                    if (++load_group == groups) start_item();
+                    load_scales(buffer ^ 1);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        sw[i] = *reinterpret_cast<const u32x4*>(scales + (buffer * ROWS + BM + (wn * NT + i) * 32 + c) * 16) >> (8 * half);
+                    }
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        sa[j] = *reinterpret_cast<const u32x4*>(scales + (buffer * ROWS + (wm * MT + j) * 32 + c) * 16) >> (8 * half);
+                    }
+                } else {
+                    load_codes(s - 1);
+                }
+                if (s == kGroupSteps - 1) store_scales(buffer ^ 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    u32x4 w[NT], x[MT];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        w[i] = *reinterpret_cast<const u32x4*>(lds + s * STAGE + (BM + (wn * NT + i) * 32) * 64 + read_at[t]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        x[j] = *reinterpret_cast<const u32x4*>(lds + s * STAGE + ((wm * MT + j) * 32) * 64 + read_at[t]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            if (t == 0) {
+                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                    operand(w[i]), operand(x[j]), acc[i][j], kE2M1, kE2M1, 0, (int)sw[i][s], 0, (int)sa[j][s]);
+                            } else {
+                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                    operand(w[i]), operand(x[j]), acc[i][j], kE2M1, kE2M1, 2, (int)sw[i][s], 2, (int)sa[j][s]);
+                            }
+                        }
+                    }
+                }
+            }
+            buffer ^= 1;
+        }
+        // lane (c, half) holds row 32 j + c of its block and, in register r, column
+        // 8 (r / 4) + 4 half + r % 4
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int m = (wm * MT + j) * 32 + c;
+            if (m >= tile.n) continue;
+            bool bad = false;
+            if (a.sorted_routes) {
+                const int route = a.sorted_routes[tile.row0 + m];
+                bad = route < 0 || route / a.top_k >= a.a_rows;
+            }
+            Raw* out = (Raw*)a.out + (int64_t)(tile.row0 + m) * a.N;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int n = tile.n0 + (wn * NT + i) * 32;
+                store_block<DT>(out, n, a.N, half, acc[i][j], bad);
+            }
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS behind the workgroup's end
+}
+
+template <int DT, int MT, int NT, int WM, int WN>
+hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
+{
+    const dim3 grid(256 * wgs_per_cu), block(64 * WM * WN);
+    const bool whole = a.K % 512 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
+    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, true>, grid, block, s, a);
+    else launch(tiled_kernel<DT, MT, NT, WM, WN, false>, grid, block, s, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s)
 {
+    if (a.a_rows * (a.K / 2) < (int64_t(1) << 31) && a.rows >= 256) {
+        if (a.dtype == kF32) return launch_tiled<kF32, 2, 4, 4, 2>(a, 1, s);
+        if (a.dtype == kBF16) return launch_tiled<kBF16, 2, 4, 4, 2>(a, 1, s);
+        return launch_tiled<kF16, 2, 4, 4, 2>(a, 1, s);
+    }
     // one partial tile at most for every expert with rows and for the rows behind
     const int64_t groups = a.offsets ? (a.E + 1 < a.rows ? a.E + 1 : a.rows) : 1;
     const int64_t tiles = (a.rows + 31) / 32 + groups;
