@@ -433,7 +433,7 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *   sorted_routes      NULL: src(r) = r (a_rows >= rows); or int32 [rows]:
  *                      src(r) = sorted_routes[r] / top_k, so tokens quantised
  *                      once serve all their routes; an entry that leads
- *                      outside [0, a_rows) gives a row of zeros
+ *                      outside [0, a_rows) stands for a row of zeros
  *   top_k              >= 1, used with sorted_routes
  *   out                dtype [rows, N] out (F16, BF16 or F32)
  * Scales of 255 (NaN) make the outputs they enter NaN.  Requires 1 <= E <=

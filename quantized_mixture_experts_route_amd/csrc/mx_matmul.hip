@@ -85,21 +85,22 @@ __global__ __launch_bounds__(256) void product_kernel(MxMatmulArgs a)
             u32x4 x = {}, w = {};
             int sx = 0, sw = 0;
             if (b < blocks) {
-                x = *reinterpret_cast<const u32x4*>(ac + b * 16);
+                if (row_ok) {
+                    x = *reinterpret_cast<const u32x4*>(ac + b * 16);
+                    sx = as[b];
+                }
                 w = *reinterpret_cast<const u32x4*>(wc + b * 16);
-                sx = as[b];
                 sw = ws[b];
             }
             acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(x), operand(w), acc, kE2M1, kE2M1, 0, sx, 0, sw);
         }
     }
-    const uint64_t ok = __ballot(row_ok);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int r = 8 * (i / 4) + 4 * half + i % 4;
         if (r < tile.n && n0 + c < a.N) {
             ((Raw*)a.out)[(int64_t)(tile.row0 + r) * a.N + n0 + c] =
-                RowType<DT>::round((ok >> r) & 1 ? acc[i] : 0.0f);
+                RowType<DT>::round(acc[i]);
         }
     }
 }
@@ -110,25 +111,32 @@ __global__ __launch_bounds__(256) void product_kernel(MxMatmulArgs a)
 // instruction's first operand, so a lane's registers run along n and its
 // results leave as 16-byte stores.
 //
-// K runs in steps of 128 values: 64 bytes of codes a row, written to LDS by
-// the load itself (buffer_load ... lds) into one of kStages stages, three
-// steps ahead.  A group of four steps needs 16 bytes of scales a row, loaded
-// one group ahead into one of two buffers; a lane reads the 16 bytes once a
-// group and picks its byte by shift and operand select.  One barrier a step:
-// it tells that the step's stage has landed and that the stage read before is
-// free.  Loads run on over the end of a tile into the workgroup's next one, so
-// only its first tile waits for memory.
+// K runs in steps of 256 values: 128 bytes of codes a row, a whole cache line
+// (64-byte pieces read every line twice from L2), written to LDS by the load
+// itself (buffer_load ... lds) into one of two stages.  A step is four
+// quarters of 64 values; a quarter's operands are read while the matrix
+// instructions of the quarter before run.  The one barrier of a step stands
+// before its last quarter: then every operand of the step is in registers, its
+// stage takes the loads of the step after the next, and the next step has
+// landed.  Loads run on over the end of a tile into the workgroup's next one,
+// so only its first tile waits for memory.
 //
-// LDS rows are 64 bytes (16 banks); the 16-byte chunk of row r sits in slot
-// chunk ^ (r / 4 % 4), so that 16 rows read at one chunk cover all 64 banks.
+// A group of four steps needs 32 bytes of scales a row, in one buffer: its last
+// read is behind the group's second barrier, so the next group's load is
+// issued behind the third and has landed at the fourth.  A lane reads 8 bytes a
+// step and picks its byte by shift and operand select.
 //
-// WHOLE: K is a multiple of 512 and the scale rows are 16-byte aligned, so
+// LDS rows are 128 bytes (32 banks); the 16-byte chunk of row r sits in slot
+// chunk ^ (r / 2 % 8), so that 16 rows read at one chunk cover all 64 banks.
+//
+// WHOLE: K is a multiple of 1024 and the scale rows are 16-byte aligned, so
 // scales take the direct path to LDS too and no step has a tail.  Otherwise
 // scales go through registers, byte by byte at the end of a row, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
-constexpr int kStages = 4;
-constexpr int kStepBytes = 64;   // codes of one row and step
-constexpr int kGroupSteps = 4;   // steps whose scales are loaded together: 16 bytes a row
+constexpr int kStages = 2;
+constexpr int kStepBytes = 128;  // codes of one row and step
+constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
+constexpr int kScaleBytes = 32;  // ... and their bytes a row
 constexpr uint32_t kOutside = 0x80000000u;  // a byte offset behind every buffer
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
@@ -154,52 +162,63 @@ __device__ inline uint32_t pack_pair(float lo, float hi)
     }
 }
 
-// A lane's 16 results of one block: columns n + 8 q + 4 half + (0..3) of its row.
-template <int DT>
-__device__ inline void store_block(typename RowType<DT>::Raw* out, int n, int N, int half, const f32x16& acc, bool zero)
+// Stores one block of 32 x 32 results: lane (c, half) holds row c, columns
+// 8 q + 4 half + i in register 4 q + i.  `out` is the block's first row and
+// column; rows and cols say how many of them exist (WHOLE: all 32).
+template <int DT, bool WHOLE>
+__device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int rows, int cols, const f32x16& acc)
 {
     typedef typename RowType<DT>::Raw Raw;
+    constexpr int V = 16 / sizeof(Raw);
+    const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
+    auto store = [&](int row, int col, const u32x4& v) {
+        if (!WHOLE && row >= rows) return;
+        RowVec<Raw, V> y;
+        __builtin_memcpy(&y, &v, 16);
+        Raw* p = out + (int64_t)row * N + col;
+        if (WHOLE || col + V <= cols) {
+            store_vec<Raw, V>(p, y);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (col + i < cols) p[i] = y.v[i];
+            }
+        }
+    };
     if constexpr (DT == kF32) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int at = n + 8 * q + 4 * half;
-            RowVec<float, 4> v;
+            u32x4 v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v.v[i] = zero ? 0.0f : acc[4 * q + i];
-            if (at + 4 <= N) {
-                store_vec<float, 4>(out + at, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (at + i < N) out[at + i] = v.v[i];
-                }
-            }
+            for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(uint32_t, (float)acc[4 * q + i]);
+            store(c, 8 * q + 4 * half, v);
         }
     } else {
-        // the halves trade four columns, so that each lane holds eight neighbours
+        // the halves trade four columns, so that each lane holds eight neighbours: v[0] columns
+        // 8 half .. 8 half + 7, v[1] the same 16 further on
+        u32x4 v[2];
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            uint32_t v[4];
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const auto sw = __builtin_amdgcn_permlane32_swap(
-                    pack_pair<DT>(acc[4 * q + 2 * i], acc[4 * q + 2 * i + 1]),
-                    pack_pair<DT>(acc[4 * q + 4 + 2 * i], acc[4 * q + 5 + 2 * i]), false, false);
-                v[i] = zero ? 0u : sw[0];
-                v[2 + i] = zero ? 0u : sw[1];
-            }
-            const int at = n + 8 * q + 8 * half;
-            RowVec<Raw, 8> y;
-            __builtin_memcpy(&y, v, 16);
-            if (at + 8 <= N) {
-                store_vec<Raw, 8>(out + at, y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (at + i < N) out[at + i] = y.v[i];
-                }
+                const auto t = __builtin_amdgcn_permlane32_swap(
+                    pack_pair<DT>(acc[8 * q + 2 * i], acc[8 * q + 2 * i + 1]),
+                    pack_pair<DT>(acc[8 * q + 4 + 2 * i], acc[8 * q + 5 + 2 * i]), false, false);
+                v[q][i] = t[0];
+                v[q][2 + i] = t[1];
             }
         }
+        // then rows 16..31 trade with rows 0..15: a store writes 16 rows of 64 neighbouring bytes
+        // (32 rows of 32 bytes took the large prefill's product from 600 to 640 us)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto t = __builtin_amdgcn_permlane16_swap(v[0][i], v[1][i], false, false);
+            v[0][i] = t[0];
+            v[1][i] = t[1];
+        }
+        const int col = 8 * half + 16 * ((lane >> 4) & 1);
+        store(lane & 15, col, v[0]);
+        store(16 + (lane & 15), col, v[1]);
     }
 }
 
@@ -265,23 +284,25 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     typedef typename RowType<DT>::Raw Raw;
     constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN, ROWS = BM + BN;
     constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
-    constexpr int LOADS = ROWS / 16 / WAVES;    // code loads of a wavefront and step: 16 rows each
-    constexpr int LOADS_A = BM / 16 / WAVES;
-    constexpr int SCALE_LOADS = (ROWS / 64 + WAVES - 1) / WAVES;  // scale loads: 64 rows each
-    static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0 && BM % 64 == 0 && BN % 64 == 0, "load split");
+    constexpr int LOADS = ROWS / 8 / WAVES;     // code loads of a wavefront and step: 8 rows each
+    constexpr int LOADS_A = BM / 8 / WAVES;
+    constexpr int SCALE_LOADS = (ROWS / 32 + WAVES - 1) / WAVES;  // scale loads: 32 rows each
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && WAVES % 2 == 0, "load split");
 
     // one array for all of it: between arrays of their own the compiler tells apart what a load to
     // LDS writes and waits for every such load before it reads LDS
-    constexpr int STAGE = ROWS * kStepBytes, SCALES = kStages * STAGE, LIST = SCALES + 2 * ROWS * 16;
-    __shared__ __align__(16) uint8_t lds[LIST + (kMaxExperts + 1) * 4];
+    constexpr int STAGE = ROWS * kStepBytes, SCALES = kStages * STAGE, LIST = SCALES + ROWS * kScaleBytes;
+    constexpr int SOURCE = LIST + (kMaxExperts + 1) * 4;
+    __shared__ __align__(16) uint8_t lds[SOURCE + BM * 4];
     uint8_t* const scales = lds + SCALES;
     int* const first = reinterpret_cast<int*>(lds + LIST);
+    int* const source = reinterpret_cast<int*>(lds + SOURCE);
 
     const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int K2 = a.K / 2, blocks = a.K / 32;
-    const int groups = (a.K + 128 * kGroupSteps - 1) / (128 * kGroupSteps);
+    const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps;  // whole groups
 
     build_tile_list<BM>(first, a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
@@ -301,76 +322,82 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         }
     }
 
-    // ---- the loading side: an item and a group, up to four steps ahead
+    // ---- the loading side: an item and a step, up to two steps ahead
     TileItem load_tile;
-    int load_group = 0;
-    uint32_t code_at[LOADS];        // byte offset of the lane's chunk at step 0
+    int load_step = 0;
+    const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+    uint32_t code_at[LOADS_A];      // byte offset of the lane's chunk at step 0
+    const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk;  // rows behind N: out of bounds
     uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's scale row
     __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
     const uint8_t* w_scale_base = nullptr;
 
-    auto a_row = [&](const TileItem& t, int r) -> int {  // source row of product row r, clamped into a
-        const int row = t.row0 + min(r, t.n - 1);
-        if (!a.sorted_routes) return row;
-        const int route = a.sorted_routes[row];
-        const int src = route / a.top_k;
-        return route < 0 || src >= a.a_rows ? 0 : src;
+    // The next item, and in LDS its rows' source rows in a (-1: outside; rows behind the tile's
+    // repeat its last).  Found while no product is pending: registers are free then, and the reads
+    // wait for nothing but loads of the tile's own last steps.
+    TileItem next_tile;
+    auto find_item = [&]() {
+        next_tile = item_at<BM, BN>(first, a.offsets, a.E, a.rows, n_tiles, next_item, end);
+        next_item += per_die;
+        for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
+            int src = next_tile.row0 + min(r, next_tile.n - 1);
+            if (a.sorted_routes) {
+                const int route = a.sorted_routes[src];
+                src = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
+            }
+            source[r] = src;
+        }
     };
     auto start_item = [&]() {
-        load_tile = item_at<BM, BN>(first, a.offsets, a.E, a.rows, n_tiles, next_item, end);
-        next_item += per_die;
-        load_group = 0;
+        load_tile = next_tile;
+        load_step = 0;
         const TileItem& t = load_tile;
         const bool on = t.n > 0;
         const int w_rows = on ? min(BN, a.N - t.n0) : 0;
-        const int64_t w0 = (int64_t)t.expert * a.N + t.n0;
+        const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
         a_buf = buffer_of(a.a_codes, on ? (uint32_t)(a.a_rows * K2) : 0u);
         w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
         as_buf = buffer_of(a.a_scales, on ? (uint32_t)(a.a_rows * blocks) : 0u);
         ws_buf = buffer_of(a.w_scales + w0 * blocks, (uint32_t)(w_rows * blocks));
         w_scale_base = a.w_scales + w0 * blocks;
-        const uint32_t chunk = (uint32_t)((lane & 3) ^ (lane >> 4)) * 16;
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
-            const int r = (j * WAVES + wave) * 16 + (lane >> 2);
-            uint32_t row = 0;
-            if (on) row = j < LOADS_A ? a_row(t, r) : min(r - BM, w_rows - 1);
-            code_at[j] = row * K2 + chunk;
+        for (int j = 0; j < LOADS_A; ++j) {
+            const int row = source[(j * WAVES + wave) * 8 + (lane >> 3)];
+            code_at[j] = row < 0 ? kOutside : row * (uint32_t)K2 + load_chunk;
         }
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
-            const int r = (j * WAVES + wave) * 64 + lane;
-            uint32_t row = 0;
-            if (on && r < ROWS) row = r < BM ? a_row(t, r) : min(r - BM, w_rows - 1);
-            scale_at[j] = row * blocks;
+            const int r0 = (j * WAVES + wave) * 32;
+            const int row = r0 < BM ? source[r0 + (lane >> 1)] : min(r0 - BM + (lane >> 1), w_rows - 1);
+            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + (lane & 1) * 16;
         }
     };
-    // codes of step s of the loading side's group into stage s
-    auto load_codes = [&](int s) {
-        const uint32_t at = (uint32_t)(load_group * kGroupSteps + s) * kStepBytes;
+    // codes of the loading side's step into stage `stage`
+    auto load_codes = [&](int stage) {
+        const uint32_t at = (uint32_t)load_step * kStepBytes;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-            uint32_t off = code_at[j];
+            uint32_t off = j < LOADS_A ? code_at[j < LOADS_A ? j : 0] : w_at + (uint32_t)((j - LOADS_A) * WAVES * 8) * K2;
             if constexpr (!WHOLE) {
-                const uint32_t chunk = (uint32_t)((lane & 3) ^ (lane >> 4)) * 16;
-                if (at + chunk >= (uint32_t)K2) off = kOutside;
+                if (at + load_chunk >= (uint32_t)K2) off = kOutside;
             }
-            load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + s * STAGE + (j * WAVES + wave) * 16 * kStepBytes);
+            load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
         }
     };
     u32x4 scale_regs[WHOLE ? 1 : SCALE_LOADS];
-    auto load_scales = [&](int buffer) {
+    auto load_scales = [&]() {  // of the group that starts at the loading side's step
+        const int at = load_step * 8;
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
-            const int r0 = (j * WAVES + wave) * 64;
+            const int r0 = (j * WAVES + wave) * 32;
             if (r0 >= ROWS) continue;
             if constexpr (WHOLE) {
-                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], load_group * 16, scales + (buffer * ROWS + r0) * 16);
+                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], at, scales + r0 * kScaleBytes);
             } else {
                 u32x4 v = {};
-                if (load_tile.n > 0) {
-                    const uint8_t* p = (r0 < BM ? a.a_scales : w_scale_base) + scale_at[j] + load_group * 16;
-                    const int left = blocks - load_group * 16;
+                if (load_tile.n > 0 && scale_at[j] != kOutside) {
+                    const uint8_t* p = (r0 < BM ? a.a_scales : w_scale_base) + scale_at[j] + at;
+                    const int left = blocks - at - (lane & 1) * 16;
                     if (left >= 16) {
                         __builtin_memcpy(&v, p, 16);
                     } else {
@@ -387,26 +414,58 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             }
         }
     };
-    auto store_scales = [&](int buffer) {  // the register path's second half
+    auto store_scales = [&]() {  // the register path's second half
         if constexpr (!WHOLE) {
 #pragma unroll
             for (int j = 0; j < SCALE_LOADS; ++j) {
-                const int r0 = (j * WAVES + wave) * 64;
-                if (r0 < ROWS) *reinterpret_cast<u32x4*>(scales + (buffer * ROWS + r0 + lane) * 16) = scale_regs[j];
+                const int r0 = (j * WAVES + wave) * 32;
+                if (r0 < ROWS) {
+                    *reinterpret_cast<u32x4*>(scales + (r0 + (lane >> 1)) * kScaleBytes + (lane & 1) * 16) = scale_regs[j];
+                }
             }
         }
     };
-
+    find_item();
+    __syncthreads();
     start_item();
-    load_scales(0);
-    store_scales(0);
+    __syncthreads();
+    find_item();
+    load_scales();
+    store_scales();
     load_codes(0);
-    load_codes(1);
-    load_codes(2);
+    ++load_step;
 
-    const uint32_t swizzle = (c >> 2) & 3;
-    const uint32_t read_at[2] = {c * 64u + ((half ^ swizzle) * 16), c * 64u + (((2 + half) ^ swizzle) * 16)};
-    int buffer = 0;
+    // chunk 2 t + half of row c
+    uint32_t read_at[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) read_at[t] = c * (uint32_t)kStepBytes + (((2 * t + half) ^ ((c >> 1) & 7)) * 16);
+    u32x4 w[2][NT], x[2][MT];
+    u32x2 sw[2][NT], sa[2][MT];
+    auto read_codes = [&](int stage, int t) {  // operands of quarter t
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            w[t & 1][i] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + (BM + (wn * NT + i) * 32) * kStepBytes + read_at[t]);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            x[t & 1][j] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ((wm * MT + j) * 32) * kStepBytes + read_at[t]);
+        }
+    };
+    auto read_scales = [&](int to, int step) {  // of one step of the group; byte 0 and 2 of a word are the lane's
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            sw[to][i] = *reinterpret_cast<const u32x2*>(scales + (BM + (wn * NT + i) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            sa[to][j] = *reinterpret_cast<const u32x2*>(scales + ((wm * MT + j) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+        }
+    };
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    load_codes(1);
+    ++load_step;
+    read_scales(0, 0);
+    read_codes(0, 0);
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
         f32x16 acc[NT][MT];
@@ -415,72 +474,62 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
         }
-        for (int g = 0; g < groups; ++g) {
-            u32x4 sw[NT], sa[MT];
+        for (int g = 0; g < steps; g += kGroupSteps) {
 #pragma unroll
             for (int s = 0; s < kGroupSteps; ++s) {
-                // step s has landed once only the loads of the two steps behind it are left
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LOADS) : "memory");
-                if (s == 0) {
-                    load_codes(3);
-                    if (++load_group == groups) start_item();
-                    load_scales(buffer ^ 1);
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        sw[i] = *reinterpret_cast<const u32x4*>(scales + (buffer * ROWS + BM + (wn * NT + i) * 32 + c) * 16) >> (8 * half);
-                    }
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) {
-                        sa[j] = *reinterpret_cast<const u32x4*>(scales + (buffer * ROWS + (wm * MT + j) * 32 + c) * 16) >> (8 * half);
-                    }
-                } else {
-                    load_codes(s - 1);
-                }
-                if (s == kGroupSteps - 1) store_scales(buffer ^ 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    u32x4 w[NT], x[MT];
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        w[i] = *reinterpret_cast<const u32x4*>(lds + s * STAGE + (BM + (wn * NT + i) * 32) * 64 + read_at[t]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) {
-                        x[j] = *reinterpret_cast<const u32x4*>(lds + s * STAGE + ((wm * MT + j) * 32) * 64 + read_at[t]);
-                    }
+                auto multiply = [&](auto quarter) {
+                    constexpr int t = decltype(quarter)::value;
+                    if (!WHOLE && (g + s) * 256 + t * 64 >= a.K) return;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
-                            if (t == 0) {
-                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                    operand(w[i]), operand(x[j]), acc[i][j], kE2M1, kE2M1, 0, (int)sw[i][s], 0, (int)sa[j][s]);
-                            } else {
-                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                    operand(w[i]), operand(x[j]), acc[i][j], kE2M1, kE2M1, 2, (int)sw[i][s], 2, (int)sa[j][s]);
-                            }
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                operand(w[t & 1][i]), operand(x[t & 1][j]), acc[i][j], kE2M1, kE2M1, 2 * (t & 1),
+                                (int)sw[s & 1][i][t >> 1], 2 * (t & 1), (int)sa[s & 1][j][t >> 1]);
+                            // keeps the product in this place: without it the compiler moves the
+                            // products of a step behind the branches and reads that follow
+                            asm volatile("" : "+v"(acc[i][j]));
                         }
                     }
-                }
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                // reads stand before the products that they hide behind; unfenced they sink to their use
+                read_codes(s & 1, 1);
+                if (s == kGroupSteps - 1) store_scales();
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(std::integral_constant<int, 0>{});
+                read_codes(s & 1, 2);
+                if (s < kGroupSteps - 1) read_scales((s + 1) & 1, s + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(std::integral_constant<int, 1>{});
+                read_codes(s & 1, 3);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(std::integral_constant<int, 2>{});
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                read_codes((s + 1) & 1, 0);
+                if (s == kGroupSteps - 1) read_scales(0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (s == kGroupSteps - 2) load_scales();
+                load_codes(s & 1);
+                multiply(std::integral_constant<int, 3>{});
+                ++load_step;
+                if (s == 1 && load_step == steps) start_item();  // a group ends a tile: its last step is loaded here
             }
-            buffer ^= 1;
         }
-        // lane (c, half) holds row 32 j + c of its block and, in register r, column
-        // 8 (r / 4) + 4 half + r % 4
+        find_item();
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            const int m = (wm * MT + j) * 32 + c;
-            if (m >= tile.n) continue;
-            bool bad = false;
-            if (a.sorted_routes) {
-                const int route = a.sorted_routes[tile.row0 + m];
-                bad = route < 0 || route / a.top_k >= a.a_rows;
-            }
-            Raw* out = (Raw*)a.out + (int64_t)(tile.row0 + m) * a.N;
+            const int m0 = (wm * MT + j) * 32;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int n = tile.n0 + (wn * NT + i) * 32;
-                store_block<DT>(out, n, a.N, half, acc[i][j], bad);
+                Raw* out = (Raw*)a.out + (int64_t)(tile.row0 + m0) * a.N + n;
+                if (tile.n - m0 >= 32 && a.N - n >= 32) {
+                    store_block<DT, true>(out, a.N, 32, 32, acc[i][j]);
+                } else {
+                    store_block<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j]);
+                }
             }
         }
     }
@@ -491,7 +540,7 @@ template <int DT, int MT, int NT, int WM, int WN>
 hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 {
     const dim3 grid(256 * wgs_per_cu), block(64 * WM * WN);
-    const bool whole = a.K % 512 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
+    const bool whole = a.K % 1024 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
     if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, true>, grid, block, s, a);
     else launch(tiled_kernel<DT, MT, NT, WM, WN, false>, grid, block, s, a);
