@@ -437,7 +437,8 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *   top_k              >= 1, used with sorted_routes
  *   out                dtype [rows, N] out (F16, BF16 or F32)
  * Scales of 255 (NaN) make the outputs they enter NaN.  Requires 1 <= E <=
- * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24.  rows = 0
+ * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24, and with
+ * sorted_routes a_rows * K/2 < 2^31 (else QMOE_ERR_UNSUPPORTED).  rows = 0
  * returns QMOE_OK and enqueues nothing.
  */
 int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,

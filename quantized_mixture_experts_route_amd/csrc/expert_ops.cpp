@@ -287,6 +287,9 @@ int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_ro
     if (rows >= (int64_t(1) << 24)) {
         return set_error(QMOE_ERR_UNSUPPORTED, "rows=%lld must be below 2^24", (long long)rows);
     }
+    if (sorted_routes && a_rows > INT32_MAX / (K / 2)) {
+        return set_error(QMOE_ERR_UNSUPPORTED, "a_codes read through sorted_routes must be below 2^31 bytes");
+    }
     if (rows == 0) return finish(hipSuccess, "");
     if (a_rows == 0) return set_error(QMOE_ERR_INVALID_ARG, "a_rows is 0");
     QMOE_TRY(check_mx("a", a_codes, a_scales));

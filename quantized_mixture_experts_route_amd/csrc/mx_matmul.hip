@@ -25,86 +25,6 @@ __device__ inline i32x8 operand(u32x4 v)
     return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
 
-// A row tile of one expert: rows [row0, row0 + n) of the product.
-struct RowTile {
-    int expert;  // E: the rows behind the last expert's
-    int row0;
-    int n;
-};
-
-// Tile `index` of the list that cuts every expert's rows, and then the rows
-// behind them, into tiles of MT rows; n = 0 past the list's end.  Offsets are
-// clamped to [0, rows], so no table content leads outside the output.
-template <int MT>
-__device__ RowTile find_tile(const int32_t* offsets, int E, int rows, int index)
-{
-    int left = index;
-    if (offsets == nullptr) {
-        const int row0 = left * MT;
-        return RowTile{0, row0, row0 < rows ? min(MT, rows - row0) : 0};
-    }
-    int at = 0;
-    for (int e = 0; e <= E; ++e) {
-        const int lo = min(max(offsets[e], 0), rows);
-        const int hi = e < E ? min(max(offsets[e + 1], lo), rows) : rows;
-        const int tiles = (hi - lo + MT - 1) / MT;
-        if (left < tiles) {
-            at = lo + left * MT;
-            return RowTile{e, at, min(MT, hi - at)};
-        }
-        left -= tiles;
-    }
-    return RowTile{E, 0, 0};
-}
-
-// One wavefront computes 32 rows x 32 columns with operands straight from
-// global memory; four wavefronts take neighbouring column blocks.
-template <int DT>
-__global__ __launch_bounds__(256) void product_kernel(MxMatmulArgs a)
-{
-    typedef typename RowType<DT>::Raw Raw;
-    const RowTile tile = find_tile<32>(a.offsets, a.E, a.rows, blockIdx.x);
-    if (tile.n <= 0) return;
-    const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
-    const int n0 = (blockIdx.y * 4 + (threadIdx.x >> 6)) * 32;
-    if (n0 >= a.N) return;
-    const int row = tile.row0 + min(c, tile.n - 1);
-    const int col = min(n0 + c, a.N - 1);
-    const int route = a.sorted_routes ? a.sorted_routes[row] : row;
-    const int64_t src = a.sorted_routes ? route / a.top_k : route;
-    const bool row_ok = route >= 0 && src < a.a_rows;
-    const int blocks = a.K / 32;
-    f32x16 acc = {};
-    if (tile.expert < a.E) {
-        const uint8_t* ac = a.a_codes + (row_ok ? src : 0) * (int64_t)(a.K / 2);
-        const uint8_t* as = a.a_scales + (row_ok ? src : 0) * (int64_t)blocks;
-        const int64_t wrow = (int64_t)tile.expert * a.N + col;
-        const uint8_t* wc = a.w_codes + wrow * (a.K / 2);
-        const uint8_t* ws = a.w_scales + wrow * blocks;
-        for (int b = half; b < blocks + half; b += 2) {
-            u32x4 x = {}, w = {};
-            int sx = 0, sw = 0;
-            if (b < blocks) {
-                if (row_ok) {
-                    x = *reinterpret_cast<const u32x4*>(ac + b * 16);
-                    sx = as[b];
-                }
-                w = *reinterpret_cast<const u32x4*>(wc + b * 16);
-                sw = ws[b];
-            }
-            acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(x), operand(w), acc, kE2M1, kE2M1, 0, sx, 0, sw);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = 8 * (i / 4) + 4 * half + i % 4;
-        if (r < tile.n && n0 + c < a.N) {
-            ((Raw*)a.out)[(int64_t)(tile.row0 + r) * a.N + n0 + c] =
-                RowType<DT>::round(acc[i]);
-        }
-    }
-}
-
 // ---------------------------------------------------------------- tiled kernel
 // A workgroup of WM x WN wavefronts computes BM = 32 MT WM rows against
 // BN = 32 NT WN weight rows; a wavefront MT x NT blocks of 32 x 32.  W is the
@@ -223,29 +143,33 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
 }
 
 // m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
-template <int BM>
-__device__ void build_tile_list(int* first, const int32_t* offsets, int E, int rows)
+// Offsets are clamped to [0, rows], so no table content leads outside the
+// output.  scratch: E + 1 words of LDS.
+template <int BM, int THREADS>
+__device__ void build_tile_list(int* first, int* scratch, const int32_t* offsets, int E, int rows)
 {
+    for (int e = threadIdx.x; e <= E; e += THREADS) {
+        scratch[e] = offsets ? min(max(offsets[e], 0), rows) : e * rows;
+    }
+    __syncthreads();
     if (threadIdx.x < kWave) {
-        int carry = 0;
-        for (int base = 0; base < E; base += kWave) {
-            const int e = base + (int)threadIdx.x;
-            int tiles = 0;
-            if (e < E) {
-                const int lo = offsets ? min(max(offsets[e], 0), rows) : 0;
-                const int hi = offsets ? min(max(offsets[e + 1], lo), rows) : rows;
-                tiles = (hi - lo + BM - 1) / BM;
-            }
-            int incl = tiles;
+        const int lane = threadIdx.x, per = (E + kWave - 1) / kWave;  // consecutive experts a lane
+        auto tiles = [&](int e) { return e < E ? (max(scratch[e + 1] - scratch[e], 0) + BM - 1) / BM : 0; };
+        int sum = 0;
+        for (int i = 0; i < per; ++i) sum += tiles(lane * per + i);
+        int incl = sum;
 #pragma unroll
-            for (int d = 1; d < kWave; d <<= 1) {
-                const int y = __shfl_up(incl, d, kWave);
-                if ((int)threadIdx.x >= d) incl += y;
-            }
-            if (e < E) first[e] = carry + incl - tiles;
-            carry += __shfl(incl, kWave - 1, kWave);
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int y = __shfl_up(incl, d, kWave);
+            if (lane >= d) incl += y;
         }
-        if (threadIdx.x == 0) first[E] = carry;
+        int run = incl - sum;
+        for (int i = 0; i < per; ++i) {
+            const int e = lane * per + i;
+            if (e < E) first[e] = run;
+            run += tiles(e);
+        }
+        if (lane == kWave - 1) first[E] = run;
     }
     __syncthreads();
 }
@@ -304,7 +228,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const int K2 = a.K / 2, blocks = a.K / 32;
     const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps;  // whole groups
 
-    build_tile_list<BM>(first, a.offsets, a.E, a.rows);
+    build_tile_list<BM, THREADS>(first, reinterpret_cast<int*>(lds), a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
     const int total = first[a.E] * n_tiles;
     // workgroups go to the 8 dies in turn: each die takes one run of items, so
@@ -330,19 +254,19 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk;  // rows behind N: out of bounds
     uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's scale row
     __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
-    const uint8_t* w_scale_base = nullptr;
+    const uint8_t *a_scale_base = nullptr, *w_scale_base = nullptr;
 
-    // The next item, and in LDS its rows' source rows in a (-1: outside; rows behind the tile's
-    // repeat its last).  Found while no product is pending: registers are free then, and the reads
+    // The next item, and in LDS its rows' source rows in a (from the tile's first row where there
+    // are no routes; -1: outside; rows behind the tile's repeat its last).  Found while no product is pending: registers are free then, and the reads
     // wait for nothing but loads of the tile's own last steps.
     TileItem next_tile;
     auto find_item = [&]() {
         next_tile = item_at<BM, BN>(first, a.offsets, a.E, a.rows, n_tiles, next_item, end);
         next_item += per_die;
         for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
-            int src = next_tile.row0 + min(r, next_tile.n - 1);
+            int src = min(r, next_tile.n - 1);
             if (a.sorted_routes) {
-                const int route = a.sorted_routes[src];
+                const int route = a.sorted_routes[next_tile.row0 + src];
                 src = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
             }
             source[r] = src;
@@ -355,9 +279,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         const bool on = t.n > 0;
         const int w_rows = on ? min(BN, a.N - t.n0) : 0;
         const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
-        a_buf = buffer_of(a.a_codes, on ? (uint32_t)(a.a_rows * K2) : 0u);
+        const int64_t a0 = a.sorted_routes ? 0 : t.row0;
+        const int64_t a_rows = !on ? 0 : a.sorted_routes ? a.a_rows : t.n;
+        a_buf = buffer_of(a.a_codes + a0 * K2, (uint32_t)(a_rows * K2));
         w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
-        as_buf = buffer_of(a.a_scales, on ? (uint32_t)(a.a_rows * blocks) : 0u);
+        a_scale_base = a.a_scales + a0 * blocks;
+        as_buf = buffer_of(a_scale_base, (uint32_t)(a_rows * blocks));
         ws_buf = buffer_of(a.w_scales + w0 * blocks, (uint32_t)(w_rows * blocks));
         w_scale_base = a.w_scales + w0 * blocks;
 #pragma unroll
@@ -396,7 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             } else {
                 u32x4 v = {};
                 if (load_tile.n > 0 && scale_at[j] != kOutside) {
-                    const uint8_t* p = (r0 < BM ? a.a_scales : w_scale_base) + scale_at[j] + at;
+                    const uint8_t* p = (r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at;
                     const int left = blocks - at - (lane & 1) * 16;
                     if (left >= 16) {
                         __builtin_memcpy(&v, p, 16);
@@ -536,34 +463,53 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS behind the workgroup's end
 }
 
+constexpr int kCUs = 256;
+
+// wgs_per_cu: as many as fit by LDS and registers.
 template <int DT, int MT, int NT, int WM, int WN>
 hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 {
-    const dim3 grid(256 * wgs_per_cu), block(64 * WM * WN);
+    constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
+    // at most one partial tile for every expert with rows
+    const int64_t experts = a.E < a.rows ? a.E : a.rows;
+    const int64_t items = (experts + (a.rows - experts) / BM) * ((a.N + BN - 1) / BN);
+    int64_t grid = (items + 7) / 8 * 8;
+    if (grid > kCUs * wgs_per_cu) grid = kCUs * wgs_per_cu;
     const bool whole = a.K % 1024 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
-    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, true>, grid, block, s, a);
-    else launch(tiled_kernel<DT, MT, NT, WM, WN, false>, grid, block, s, a);
+    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
+    else launch(tiled_kernel<DT, MT, NT, WM, WN, false>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
     return hipGetLastError();
+}
+
+// Tile by the mean rows of an expert that has some and by how many tiles that
+// makes; measured with E = 8, N = 4096, K = 2048 unless said otherwise, us:
+//   rows   8: 32x64   7.7, 64x128   8.9       rows  128: 32x64 10.6, 64x128 11.7
+//   rows 512: 64x128 13.5, 128x128 15.4       rows 1024: 64x128 22.0, 128x128 17.2
+//   rows 8192: 128x128 62.5, 256x256 72.4 (576 tiles of 256 x 256 for 256 CUs)
+//   rows 8192, K 4096, N 8192: 128x128 205, 256x256 188 (1152 tiles)
+//   rows 1024, E = 1, N = 2048: 64x128 8.7, 128x128 10.0 (too few tiles)
+template <int DT>
+hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
+{
+    const int64_t experts = a.E < a.rows ? a.E : a.rows;
+    const int64_t mean = a.rows / experts;
+    auto tiles = [&](int bm, int bn) {  // an expert's last tile counts half
+        return (a.rows / bm + experts / 2 + 1) * ((a.N + bn - 1) / bn);
+    };
+    if (mean <= 16) return launch_tiled<DT, 1, 1, 1, 2>(a, 5, s);
+    if (mean <= 64 || tiles(128, 128) < kCUs) return launch_tiled<DT, 1, 2, 2, 2>(a, 2, s);
+    if (tiles(256, 256) < 5 * kCUs / 2) return launch_tiled<DT, 2, 2, 2, 2>(a, 2, s);
+    return launch_tiled<DT, 2, 4, 4, 2>(a, 1, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx_matmul(const MxMatmulArgs& a, hipStream_t s)
 {
-    if (a.a_rows * (a.K / 2) < (int64_t(1) << 31) && a.rows >= 256) {
-        if (a.dtype == kF32) return launch_tiled<kF32, 2, 4, 4, 2>(a, 1, s);
-        if (a.dtype == kBF16) return launch_tiled<kBF16, 2, 4, 4, 2>(a, 1, s);
-        return launch_tiled<kF16, 2, 4, 4, 2>(a, 1, s);
-    }
-    // one partial tile at most for every expert with rows and for the rows behind
-    const int64_t groups = a.offsets ? (a.E + 1 < a.rows ? a.E + 1 : a.rows) : 1;
-    const int64_t tiles = (a.rows + 31) / 32 + groups;
-    const dim3 grid((unsigned)tiles, (unsigned)((a.N + 127) / 128));
-    if (a.dtype == kF32) launch(product_kernel<kF32>, grid, dim3(256), s, a);
-    else if (a.dtype == kBF16) launch(product_kernel<kBF16>, grid, dim3(256), s, a);
-    else launch(product_kernel<kF16>, grid, dim3(256), s, a);
-    return hipGetLastError();
+    if (a.dtype == kF32) return launch_by_shape<kF32>(a, s);
+    if (a.dtype == kBF16) return launch_by_shape<kBF16>(a, s);
+    return launch_by_shape<kF16>(a, s);
 }
 
 }  // namespace qmoe
