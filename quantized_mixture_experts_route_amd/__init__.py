@@ -424,6 +424,8 @@ def raw_codes(proj: Projection, E: int, N: int, K: int, block_size: int, dtype: 
 
 
 # ------------------------------------------------ sorted by expert and back, MXFP4
+# One call of these takes a few microseconds on the GPU, so the binding's own time counts: a tensor
+# that is right passes one comparison, and the message is worked out only for one that is not.
 _ROW_DTYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 
@@ -434,52 +436,68 @@ def _row_dtype(dt: torch.dtype, name: str) -> int:
     return code
 
 
-def _tensor(t, name: str, device, dtype=None, shape=None) -> torch.Tensor:
-    """_dev for the operators below: also on `device` (that of the call's first tensor)."""
-    _dev(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
-
-
-def _rows(t, name: str, device=None) -> int:
-    """Checks a matrix of rows (any row stride, neighbouring elements); its row stride."""
+def _device(t, name: str, dim: int) -> torch.device:
+    """The device of a call's leading tensor, which must have `dim` dimensions."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if device is not None and t.device != device:
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    return t.device
+
+
+def _tensor(t, name: str, device, dtype, shape) -> int:
+    """Checks a contiguous tensor on `device`; its address."""
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _dev(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    n, h = t.shape
+    return t.data_ptr()
+
+
+def _rows(t, name: str, device, n: int) -> int:
+    """Checks a matrix of n rows (any row stride, neighbouring elements); its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} rows")
+    h = t.shape[1]
     if h < 1:
         raise ValueError(f"{name} has no columns")
-    if h > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < h:
+    if n <= 1:
+        if h > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return h
+    stride, step = t.stride()
+    if h > 1 and step != 1 or stride < h:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
-    return t.stride(0) if n > 1 else h
+    return stride
 
 
-class _On:
-    """The device and the stream of a call: outputs are allocated for the stream that fills them,
-    and the launch goes to the tensors' device whichever is current."""
+def _elsewhere(device, stream) -> bool:
+    """Whether a call must be made under _on(): on a given stream or not on the current device."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.raw = self.stream.cuda_stream
-        # torch.cuda.stream() also makes the stream's device current
-        plain = stream is None and device.index == torch.cuda.current_device()
-        self._context = None if plain else torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        if self._context is not None:
-            self._context.__enter__()
-        return self
+def _on(device, stream):
+    """Makes the device and the stream current, so that outputs are allocated for the stream that
+    fills them and the launch goes to the tensors' device."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+    return torch.cuda.stream(stream)
 
-    def __exit__(self, *exc):
-        if self._context is not None:
-            self._context.__exit__(*exc)
-        return False
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(device) -> int:
+    """The handle of the current stream (without the Stream object, which costs microseconds)."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def permute_workspace_size(T: int, top_k: int, E: int) -> int:
@@ -494,59 +512,50 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
     hidden: float16, bfloat16 or float32 [T, H], any row stride; None: rows is None and only the
     maps are made.  Ids outside [0, E) drop their route: its row, behind the last expert's, is zero
     and its route_rows entry is -1 - row."""
-    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
-        raise ValueError("topk_ids must be a tensor [T, top_k]")
-    dev = topk_ids.device
-    _dev(topk_ids, "topk_ids", torch.int32)
+    dev = _device(topk_ids, "topk_ids", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return permute(hidden, topk_ids, E, workspace=workspace)
     T, top_k = topk_ids.shape
-    stride, H, dt = 0, 0, DTYPE_F16
-    if hidden is not None:
-        stride, H, dt = _rows(hidden, "hidden", dev), hidden.shape[1], _row_dtype(hidden.dtype, "hidden")
-        if hidden.shape[0] != T:
-            raise ValueError(f"hidden has {hidden.shape[0]} rows, topk_ids {T}")
-    lib = load_library()
     R = T * top_k
-    with _On(dev, stream) as on:
-        if workspace is None:
-            need = lib.qmoe_permute_workspace_size(T, top_k, E)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _tensor(workspace, "workspace", dev, torch.uint8)
-        rows = None if hidden is None else torch.empty((R, H), dtype=hidden.dtype, device=dev)
-        maps = torch.empty(max(E, 0) + 1 + 2 * R, dtype=torch.int32, device=dev)
-        offsets, order, route_rows = maps[:E + 1], maps[E + 1:E + 1 + R], maps[E + 1 + R:].view(T, top_k)
-        _check(lib.qmoe_permute(_ptr(hidden), stride, T, H, dt, _ptr(topk_ids), top_k, E, _ptr(rows),
-                                _ptr(offsets), _ptr(order), _ptr(route_rows), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(), on.raw))
+    ids = _tensor(topk_ids, "topk_ids", dev, torch.int32, (T, top_k))
+    stride, H, dt, rows = 0, 0, DTYPE_F16, None
+    if hidden is not None:
+        stride, H, dt = _rows(hidden, "hidden", dev, T), hidden.shape[1], _row_dtype(hidden.dtype, "hidden")
+        rows = hidden.new_empty((R, H))
+    lib = load_library()
+    need = lib.qmoe_permute_workspace_size(T, top_k, E)
+    if workspace is not None:
+        _tensor(workspace, "workspace", dev, torch.uint8, workspace.shape)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    offsets = topk_ids.new_empty((max(E, 0) + 1,))
+    order = topk_ids.new_empty((R,))
+    route_rows = torch.empty_like(topk_ids)
+    _check(lib.qmoe_permute(_ptr(hidden), stride, T, H, dt, ids, top_k, E, _ptr(rows), offsets.data_ptr(),
+                            order.data_ptr(), route_rows.data_ptr(), _ptr(workspace),
+                            0 if workspace is None else workspace.numel(), _current(dev)))
     return rows, offsets, order, route_rows
-
-
-def _back_sizes(route_rows):
-    if not isinstance(route_rows, torch.Tensor) or route_rows.dim() != 2:
-        raise ValueError("route_rows must be a tensor [T, top_k]")
-    _dev(route_rows, "route_rows", torch.int32)
-    return route_rows.device, route_rows.shape[0], route_rows.shape[1]
 
 
 def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows back to their tokens: out[t] = sum over slots of weights[t, s] * rows[route_rows[t, s]]
     (float32 sums, rounded once; no weights: 1); dropped routes add nothing."""
-    dev, T, top_k = _back_sizes(route_rows)
-    stride, dt = _rows(rows, "rows", dev), _row_dtype(rows.dtype, "rows")
+    dev = _device(route_rows, "route_rows", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return unpermute(rows, route_rows, weights, out=out)
+    shape = route_rows.shape
+    T, top_k = shape
+    at = _tensor(route_rows, "route_rows", dev, torch.int32, shape)
+    stride, dt = _rows(rows, "rows", dev, T * top_k), _row_dtype(rows.dtype, "rows")
     H = rows.shape[1]
-    if rows.shape[0] != T * top_k:
-        raise ValueError(f"rows has {rows.shape[0]} rows, expected {T * top_k}")
-    if weights is not None:
-        _tensor(weights, "weights", dev, torch.float32, (T, top_k))
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((T, H), dtype=rows.dtype, device=dev)
-        else:
-            _tensor(out, "out", dev, rows.dtype, (T, H))
-        _check(load_library().qmoe_unpermute(_ptr(rows), stride, _ptr(route_rows), _ptr(weights), T, top_k,
-                                             H, dt, _ptr(out), on.raw))
+    w = None if weights is None else _tensor(weights, "weights", dev, torch.float32, shape)
+    if out is None:
+        out = rows.new_empty((T, H))
+    to = _tensor(out, "out", dev, rows.dtype, (T, H))
+    _check(load_library().qmoe_unpermute(rows.data_ptr(), stride, at, w, T, top_k, H, dt, to, _current(dev)))
     return out
 
 
@@ -560,27 +569,27 @@ def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], rou
                        weights: Optional[torch.Tensor] = None, *, stream=None):
     """The gradient of unpermute: (grad_rows [T*k, H], grad_weights float32 [T, k]).  rows None:
     grad_weights is not computed (None), as for an unpermute without weights."""
-    dev, T, top_k = _back_sizes(route_rows)
-    gstride, dt = _rows(grad_out, "grad_out", dev), _row_dtype(grad_out.dtype, "grad_out")
+    dev = _device(route_rows, "route_rows", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return unpermute_backward(grad_out, rows, route_rows, weights)
+    shape = route_rows.shape
+    T, top_k = shape
+    at = _tensor(route_rows, "route_rows", dev, torch.int32, shape)
+    gstride, dt = _rows(grad_out, "grad_out", dev, T), _row_dtype(grad_out.dtype, "grad_out")
     H = grad_out.shape[1]
-    if grad_out.shape[0] != T:
-        raise ValueError(f"grad_out has {grad_out.shape[0]} rows, expected {T}")
-    stride = 0
+    stride, grad_weights = 0, None
     if rows is not None:
-        stride = _rows(rows, "rows", dev)
-        if rows.dtype != grad_out.dtype or tuple(rows.shape) != (T * top_k, H):
+        stride = _rows(rows, "rows", dev, T * top_k)
+        if rows.dtype is not grad_out.dtype or rows.shape[1] != H:
             raise ValueError(f"rows is {rows.dtype} {tuple(rows.shape)}, expected {grad_out.dtype} "
                              f"{(T * top_k, H)}")
-    if weights is not None:
-        _tensor(weights, "weights", dev, torch.float32, (T, top_k))
-    with _On(dev, stream) as on:
-        grad_rows = torch.empty((T * top_k, H), dtype=grad_out.dtype, device=dev)
-        grad_weights = None
-        if rows is not None:
-            grad_weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        _check(load_library().qmoe_unpermute_backward(
-            _ptr(grad_out), gstride, _ptr(rows), stride, _ptr(route_rows), _ptr(weights), T, top_k, H, dt,
-            _ptr(grad_rows), _ptr(grad_weights), on.raw))
+        grad_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    w = None if weights is None else _tensor(weights, "weights", dev, torch.float32, shape)
+    grad_rows = grad_out.new_empty((T * top_k, H))
+    _check(load_library().qmoe_unpermute_backward(
+        grad_out.data_ptr(), gstride, _ptr(rows), stride, at, w, T, top_k, H, dt, grad_rows.data_ptr(),
+        _ptr(grad_weights), _current(dev)))
     return grad_rows, grad_weights
 
 
@@ -590,46 +599,50 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
     its rows, giving codes [E, K, rows/2] and scales [E, K, rows/32] of the transposed matrices."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA (HIP) tensor")
-    dt, dev = _row_dtype(x.dtype, "x"), x.device
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mx_quantize(x, transpose=transpose)
+    dt = _row_dtype(x.dtype, "x")
+    lib = load_library()
     if transpose:
         if x.dim() not in (2, 3):
             raise ValueError("x must have 2 or 3 dimensions to be quantised along its rows")
         _dev(x, "x")
-        rows, K = x.shape[-2:]
-        E = x.shape[0] if x.dim() == 3 else 1
-        lead, width = (*x.shape[:-2], K), rows
+        *lead, rows, K = x.shape
+        codes = torch.empty((*lead, K, rows // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((*lead, K, rows // MX_BLOCK), dtype=torch.uint8, device=dev)
+        _check(lib.qmoe_mx_quantize_columns(x.data_ptr(), lead[0] if lead else 1, rows, K, dt,
+                                            codes.data_ptr(), scales.data_ptr(), _current(dev)))
+        return codes, scales
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
+    *lead, K = x.shape
+    if x.dim() == 2:
+        rows = lead[0]
+        stride = _rows(x, "x", dev, rows)
     else:
-        if x.dim() < 1:
-            raise ValueError("x must have at least 1 dimension")
-        K = x.shape[-1]
-        lead, width = x.shape[:-1], K
-        if x.dim() == 2:
-            rows, stride = x.shape[0], _rows(x, "x")
-        else:
-            _dev(x, "x")
-            rows, stride = math.prod(lead), K
-    with _On(dev, stream) as on:
-        codes = torch.empty((*lead, width // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((*lead, width // MX_BLOCK), dtype=torch.uint8, device=dev)
-        lib = load_library()
-        if transpose:
-            _check(lib.qmoe_mx_quantize_columns(_ptr(x), E, rows, K, dt, _ptr(codes), _ptr(scales), on.raw))
-        else:
-            _check(lib.qmoe_mx_quantize(_ptr(x), stride, rows, K, dt, _ptr(codes), _ptr(scales), on.raw))
+        _dev(x, "x")
+        rows, stride = math.prod(lead), K
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    _check(lib.qmoe_mx_quantize(x.data_ptr(), stride, rows, K, dt, codes.data_ptr(), scales.data_ptr(),
+                                _current(dev)))
     return codes, scales
 
 
-def _mx(codes, scales, name: str, device):
-    """Checks a pair of codes [..., K/2] and scales [..., K/32]; returns K."""
-    _tensor(codes, f"{name}_codes", device, torch.uint8)
-    _tensor(scales, f"{name}_scales", device, torch.uint8)
-    if codes.dim() < 1 or scales.dim() != codes.dim() or codes.shape[:-1] != scales.shape[:-1]:
-        raise ValueError(f"{name}_codes {tuple(codes.shape)} and {name}_scales {tuple(scales.shape)} "
-                         "do not belong together")
-    K = codes.shape[-1] * 2
-    if K != scales.shape[-1] * MX_BLOCK:
-        raise ValueError(f"{name}_codes holds {K} values a row, {name}_scales {scales.shape[-1]} blocks "
-                         f"of {MX_BLOCK}")
+def _mx(codes, scales, name: str, device) -> int:
+    """Checks a pair of codes [..., K/2] and scales [..., K/32]; K."""
+    if not isinstance(codes, torch.Tensor):
+        raise ValueError(f"{name}_codes must be a CUDA (HIP) tensor")
+    shape = codes.shape
+    if len(shape) < 1:
+        raise ValueError(f"{name}_codes must have at least 1 dimension")
+    _tensor(codes, f"{name}_codes", device, torch.uint8, shape)
+    K = shape[-1] * 2
+    if K % MX_BLOCK:
+        raise ValueError(f"{name}_codes holds {K} values a row, which are no whole blocks of {MX_BLOCK}")
+    _tensor(scales, f"{name}_scales", device, torch.uint8, (*shape[:-1], K // MX_BLOCK))
     return K
 
 
@@ -637,17 +650,19 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """What MXFP4 codes [..., K/2] with scales [..., K/32] stand for, [..., K] in dtype."""
     dt = _row_dtype(dtype, "dtype")
-    _dev(codes, "codes")
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise ValueError("codes must be a CUDA (HIP) tensor")
     dev = codes.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mx_dequantize(codes, scales, dtype, out=out)
     K = _mx(codes, scales, "mx", dev)
     shape = (*codes.shape[:-1], K)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _tensor(out, "out", dev, dtype, shape)
-        _check(load_library().qmoe_mx_dequantize(_ptr(codes), _ptr(scales), math.prod(shape[:-1]), K, dt,
-                                                 _ptr(out), on.raw))
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    to = _tensor(out, "out", dev, dtype, shape)
+    _check(load_library().qmoe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), math.prod(shape[:-1]), K, dt,
+                                             to, _current(dev)))
     return out
 
 
@@ -663,30 +678,31 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     a's row sorted_routes[r] // top_k; without it row r takes a's row r.  Rows behind the last
     expert's are zero."""
     dt = _row_dtype(dtype, "dtype")
-    _dev(a_codes, "a_codes", torch.uint8)
-    dev = a_codes.device
+    dev = _device(a_codes, "a_codes", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mx_matmul(a_codes, a_scales, w_codes, w_scales, expert_offsets, sorted_routes=sorted_routes,
+                             top_k=top_k, dtype=dtype, out=out)
     K = _mx(a_codes, a_scales, "a", dev)
     if _mx(w_codes, w_scales, "w", dev) != K:
         raise ValueError(f"a has {K} values a row, w {w_codes.shape[-1] * 2}")
-    if a_codes.dim() != 2 or w_codes.dim() not in (2, 3):
-        raise ValueError("a must have 2 dimensions and w 2 or 3")
+    if w_codes.dim() not in (2, 3):
+        raise ValueError(f"w_codes must have 2 or 3 dimensions, got {w_codes.dim()}")
     E, N = (1, w_codes.shape[0]) if w_codes.dim() == 2 else w_codes.shape[:2]
+    offsets = routes = None
     if expert_offsets is not None:
-        _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
-    rows = a_codes.shape[0]
+        offsets = _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
+    A = rows = a_codes.shape[0]
     if sorted_routes is not None:
-        _tensor(sorted_routes, "sorted_routes", dev, torch.int32)
-        if sorted_routes.dim() != 1:
-            raise ValueError("sorted_routes must have 1 dimension")
+        _device(sorted_routes, "sorted_routes", 1)
         rows = sorted_routes.shape[0]
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((rows, N), dtype=dtype, device=dev)
-        else:
-            _tensor(out, "out", dev, dtype, (rows, N))
-        _check(load_library().qmoe_mx_matmul(
-            _ptr(a_codes), _ptr(a_scales), a_codes.shape[0], _ptr(w_codes), _ptr(w_scales), E, N, K,
-            _ptr(expert_offsets), _ptr(sorted_routes), top_k, rows, dt, _ptr(out), on.raw))
+        routes = _tensor(sorted_routes, "sorted_routes", dev, torch.int32, (rows,))
+    if out is None:
+        out = torch.empty((rows, N), dtype=dtype, device=dev)
+    to = _tensor(out, "out", dev, dtype, (rows, N))
+    _check(load_library().qmoe_mx_matmul(
+        a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
+        routes, top_k, rows, dt, to, _current(dev)))
     return out
 
 
