@@ -35,9 +35,69 @@ constexpr int kMaxTopK = 1024;
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int64_t kOneLaunchRoutes = 16384;
-constexpr int kSpanRoutes = 4096;
+constexpr int kSpanRoutes = 4096;  // (a span is at most that or one workgroup's tokens)
 
 __device__ inline int route_key(int id, int E) { return id >= 0 && id < E ? id : E; }
+
+// Lanes of the wavefront that hold the same key as this one, of those in `valid`.
+__device__ inline uint64_t same_key(int key, uint64_t valid, int bits)
+{
+    uint64_t peers = valid;
+    for (int i = 0; i < bits; ++i) {
+        const bool bit = (key >> i) & 1;
+        const uint64_t set = __ballot(bit);
+        peers &= bit ? set : ~set;
+    }
+    return peers;
+}
+
+// Adds the keys of routes lo .. hi (at most kMaxCounted of them) to a table in
+// LDS.  Many keys: each lane adds its own.  With up to 16 keys the lanes of a
+// wavefront would queue at a handful of words (worst where neighbouring routes
+// go to one expert), so each thread counts in bytes of two 64-bit registers,
+// and a wavefront sums those with cross-lane adds before one lane adds them.
+constexpr int kFewKeys = 16;
+constexpr int64_t kMaxCounted = 255 * kSortThreads;  // a thread's count of a key fits a byte
+static_assert(kOneLaunchRoutes <= kMaxCounted && kSpanRoutes <= kMaxCounted && kMaxTopK <= kMaxCounted, "counts");
+__device__ void count_routes(const int32_t* ids, int64_t lo, int64_t hi, int E, int* table)
+{
+    if (E >= kFewKeys) {
+        for (int64_t r = lo + threadIdx.x; r < hi; r += kSortThreads) atomicAdd(&table[route_key(ids[r], E)], 1);
+        return;
+    }
+    if (lo + (threadIdx.x & ~63) >= hi) return;  // nothing for this wavefront
+    uint64_t low = 0, high = 0;  // keys 0..7 and 8..15
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kSortThreads) {
+        const int key = route_key(ids[r], E);
+        const uint64_t one = 1ull << (8 * (key & 7));
+        if (key < 8) low += one; else high += one;
+    }
+    // pairs of 16-bit counts: a wavefront's stay below 64 * 255
+    uint32_t pair[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t word = (uint32_t)((i < 2 ? low : high) >> (32 * (i & 1)));
+        pair[2 * i] = word & 0x00ff00ffu;             // keys 4i and 4i + 2
+        pair[2 * i + 1] = (word >> 8) & 0x00ff00ffu;  // keys 4i + 1 and 4i + 3
+    }
+    const int lane = threadIdx.x & 63;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t v = pair[i];
+        v += dpp_u32<kDppXor1>(v);
+        v += dpp_u32<kDppXor2>(v);
+        v += dpp_u32<kDppHalfMirror>(v);
+        v += dpp_u32<kDppMirror>(v);
+        v = (uint32_t)__builtin_amdgcn_readlane((int)v, 0) + (uint32_t)__builtin_amdgcn_readlane((int)v, 16) +
+            (uint32_t)__builtin_amdgcn_readlane((int)v, 32) + (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+        // lane = key takes its half: pair i holds keys 4 (i/2) + i%2 and 2 more
+        const int key = 4 * (i >> 1) + (i & 1);
+        if (lane == key) mine = v & 0xffffu;
+        if (lane == key + 2) mine = v >> 16;
+    }
+    if (lane <= E && mine) atomicAdd(&table[lane], (int)mine);
+}
 
 // Exclusive scan of v[0..n), n <= kMaxExperts + 1, by the whole workgroup.
 __device__ void scan_counts(int* v, int n, int* wave_sums)
@@ -98,6 +158,20 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
     const bool spans = sh.wgs_per_span > 0;
     const int64_t span = spans ? blockIdx.x / sh.wgs_per_span : 0;
 
+    // the first vectors of the tokens' rows are on their way while the routes are counted
+    constexpr int AHEAD = V > 1 ? 4 : 1;
+    const int nvec = row_vecs<V>(H);
+    const int vecs = hidden ? tokens * nvec : 0;
+    auto load = [&](int i) {
+        const int t = i / nvec;
+        return load_vec<Raw, V>((const Raw*)hidden + (t0 + t) * row_stride + vec_start<V>(i - t * nvec, H));
+    };
+    RowVec<Raw, V> x[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+        if (tid + q * kSortThreads < vecs) x[q] = load(tid + q * kSortThreads);
+    }
+
     for (int e = tid; e <= E; e += kSortThreads) {
         before[e] = spans ? span_starts[span * (E + 1) + e] : 0;
         base[e] = spans ? totals[e] : 0;
@@ -106,9 +180,8 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
     {
         const int64_t lo = spans ? span * sh.wgs_per_span * (int64_t)sh.tokens_per_wg * top_k : 0;
         const int64_t hi = spans ? r0 : T * top_k;
-        for (int64_t r = lo + tid; r < hi; r += kSortThreads) {
-            atomicAdd(r < r0 ? &before[route_key(ids[r], E)] : &base[route_key(ids[r], E)], 1);
-        }
+        count_routes(ids, lo, r0, E, before);
+        count_routes(ids, r0, hi, E, base);
     }
     __syncthreads();
     if (!spans) {
@@ -130,12 +203,7 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
         for (int b = 0; b < routes; b += kWave) {
             const bool valid = b + lane < routes;
             const int key = valid ? route_key(ids[r0 + b + lane], E) : -1;
-            uint64_t peers = __ballot(valid);
-            for (int i = 0; i < bits; ++i) {
-                const bool bit = (key >> i) & 1;
-                const uint64_t set = __ballot(bit);
-                peers &= bit ? set : ~set;
-            }
+            const uint64_t peers = same_key(key, __ballot(valid), bits);
             if (valid) {
                 const int row = before[key] + __popcll(peers & ((1ull << lane) - 1ull));
                 row_of[b + lane] = key < E ? row : ~row;
@@ -150,15 +218,18 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
     if (hidden == nullptr) return;
     __syncthreads();
 
-    const int nvec = row_vecs<V>(H);
-    for (int i = tid; i < tokens * nvec; i += kSortThreads) {
-        const int t = i / nvec;
-        const int h = vec_start<V>(i - t * nvec, H);
-        const auto x = load_vec<Raw, V>((const Raw*)hidden + (t0 + t) * row_stride + h);
-        for (int s = 0; s < top_k; ++s) {
-            const int row = row_of[t * top_k + s];
-            Raw* dst = (Raw*)rows + (int64_t)(row < 0 ? ~row : row) * H + h;
-            store_vec<Raw, V>(dst, row < 0 ? RowVec<Raw, V>{} : x);
+    for (int i = tid; i < vecs; i += AHEAD * kSortThreads) {
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            const int j = i + q * kSortThreads;
+            if (j >= vecs) break;
+            const int t = j / nvec, h = vec_start<V>(j - t * nvec, H);
+            for (int s = 0; s < top_k; ++s) {
+                const int row = row_of[t * top_k + s];
+                Raw* dst = (Raw*)rows + (int64_t)(row < 0 ? ~row : row) * H + h;
+                store_vec<Raw, V>(dst, row < 0 ? RowVec<Raw, V>{} : x[q]);
+            }
+            if (j + AHEAD * kSortThreads < vecs) x[q] = load(j + AHEAD * kSortThreads);
         }
     }
 }
@@ -173,7 +244,7 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(const int32_t* __re
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * span_routes;
     const int64_t hi = lo + span_routes < R ? lo + span_routes : R;
-    for (int64_t r = lo + threadIdx.x; r < hi; r += kSortThreads) atomicAdd(&cnt[route_key(ids[r], E)], 1);
+    count_routes(ids, lo, hi, E, cnt);
     __syncthreads();
     for (int e = threadIdx.x; e <= E; e += kSortThreads) counts[blockIdx.x * (int64_t)(E + 1) + e] = cnt[e];
 }
@@ -366,8 +437,11 @@ SortShape sort_shape(int64_t T, int top_k)
 {
     const int64_t R = T * top_k;
     SortShape sh;
-    // about 64 routes a workgroup, fewer while that leaves CUs without one
-    int64_t per = 64 / top_k;
+    // about 64 routes a workgroup, fewer while that leaves CUs without one, more
+    // where workgroups come in many rounds
+    int64_t routes = R / 1024;
+    routes = routes < 64 ? 64 : routes > 256 ? 256 : routes;
+    int64_t per = routes / top_k;
     const int64_t spread = T / 512;
     if (spread < per) per = spread;
     sh.tokens_per_wg = per < 1 ? 1 : (int)per;
