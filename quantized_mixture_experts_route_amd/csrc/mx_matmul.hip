@@ -33,18 +33,20 @@ __device__ inline i32x8 operand(u32x4 v)
 //
 // K runs in steps of 256 values: 128 bytes of codes a row, a whole cache line
 // (64-byte pieces read every line twice from L2), written to LDS by the load
-// itself (buffer_load ... lds) into one of two stages.  A step is four
+// itself (buffer_load ... lds) into one of STAGES stages.  A step is four
 // quarters of 64 values; a quarter's operands are read while the matrix
 // instructions of the quarter before run.  The one barrier of a step stands
 // before its last quarter: then every operand of the step is in registers, its
-// stage takes the loads of the step after the next, and the next step has
-// landed.  Loads run on over the end of a tile into the workgroup's next one,
-// so only its first tile waits for memory.
+// stage takes the loads of the step STAGES ahead, and the next step has landed.
+// Loads run on over the end of a tile into the workgroup's next one, so only
+// its first tile waits for memory.  Two stages where tiles are large (LDS);
+// four where few rows leave latency as the bound.
 //
-// A group of four steps needs 32 bytes of scales a row, in one buffer: its last
-// read is behind the group's second barrier, so the next group's load is
-// issued behind the third and has landed at the fourth.  A lane reads 8 bytes a
-// step and picks its byte by shift and operand select.
+// A group of four steps needs 32 bytes of scales a row.  With two stages there
+// is one buffer: its last read is behind the group's second barrier, the next
+// group's load is issued behind the third and has landed at the fourth.  With
+// four stages there are two, loaded a group ahead.  A lane reads 8 bytes a step
+// and picks its byte by shift and operand select.
 //
 // LDS rows are 128 bytes (32 banks); the 16-byte chunk of row r sits in slot
 // chunk ^ (r / 2 % 8), so that 16 rows read at one chunk cover all 64 banks.
@@ -53,7 +55,13 @@ __device__ inline i32x8 operand(u32x4 v)
 // scales take the direct path to LDS too and no step has a tail.  Otherwise
 // scales go through registers, byte by byte at the end of a row, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
-constexpr int kStages = 2;
+//
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 600 us, 3.2
+// PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
+// instructions alone would take 354 us (power holds them at 1.8 GHz), loads
+// alone 360 us (64 KB a step and CU from L2, 12 TB/s), storing 470 MB 100 us.
+// 8192^3, one expert: 270 us, 4.1 PFLOP/s.  Few rows: HBM; 60 rows over 512
+// experts 20.9 us for 96 MB (4.6 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row
@@ -129,7 +137,6 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
             }
         }
         // then rows 16..31 trade with rows 0..15: a store writes 16 rows of 64 neighbouring bytes
-        // (32 rows of 32 bytes took the large prefill's product from 600 to 640 us)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const auto t = __builtin_amdgcn_permlane16_swap(v[0][i], v[1][i], false, false);
@@ -181,9 +188,9 @@ struct TileItem {
     int n0;  // first column
 };
 
-template <int BM, int BN>
-__device__ TileItem item_at(const int* first, const int32_t* offsets, int E, int rows, int n_tiles, int item,
-                            int end)
+// offset(e) gives expert e's clamped offset.
+template <int BM, int BN, class Offset>
+__device__ TileItem item_at(const int* first, Offset offset, int E, int n_tiles, int item, int end)
 {
     if (item >= end) return TileItem{0, 0, 0, 0};
     int lo = 0, hi = E - 1;  // the last expert whose first item is <= item
@@ -196,13 +203,12 @@ __device__ TileItem item_at(const int* first, const int32_t* offsets, int E, int
     const int m_tiles = __builtin_amdgcn_readfirstlane(first[lo + 1]) - base;
     const int local = item - base * n_tiles;
     const int nt = local / m_tiles;  // neighbouring items share the weights
-    const int r_lo = offsets ? min(max(offsets[lo], 0), rows) : 0;
-    const int r_hi = offsets ? min(max(offsets[lo + 1], r_lo), rows) : rows;
+    const int r_lo = offset(lo), r_hi = offset(lo + 1);
     const int row0 = r_lo + (local - nt * m_tiles) * BM;
     return TileItem{lo, row0, min(BM, r_hi - row0), nt * BN};
 }
 
-template <int DT, int MT, int NT, int WM, int WN, bool WHOLE>
+template <int DT, int MT, int NT, int WM, int WN, int STAGES, bool WHOLE>
 __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 {
     typedef typename RowType<DT>::Raw Raw;
@@ -215,9 +221,10 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 
     // one array for all of it: between arrays of their own the compiler tells apart what a load to
     // LDS writes and waits for every such load before it reads LDS
-    constexpr int STAGE = ROWS * kStepBytes, SCALES = kStages * STAGE, LIST = SCALES + ROWS * kScaleBytes;
-    constexpr int SOURCE = LIST + (kMaxExperts + 1) * 4;
-    __shared__ __align__(16) uint8_t lds[SOURCE + BM * 4];
+    constexpr int SCALE_BUFFERS = STAGES / 2;
+    constexpr int STAGE = ROWS * kStepBytes, SCALES = STAGES * STAGE;
+    constexpr int LIST = SCALES + SCALE_BUFFERS * ROWS * kScaleBytes, SOURCE = LIST + (kMaxExperts + 1) * 4;
+    __shared__ __align__(16) uint8_t lds[SOURCE + 2 * BM * 4];
     uint8_t* const scales = lds + SCALES;
     int* const first = reinterpret_cast<int*>(lds + LIST);
     int* const source = reinterpret_cast<int*>(lds + SOURCE);
@@ -228,7 +235,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const int K2 = a.K / 2, blocks = a.K / 32;
     const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps;  // whole groups
 
-    build_tile_list<BM, THREADS>(first, reinterpret_cast<int*>(lds), a.offsets, a.E, a.rows);
+    // the last stage's space, not loaded before the first barrier, holds the offsets for the first item
+    int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
+    build_tile_list<BM, THREADS>(first, scratch, a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
     const int total = first[a.E] * n_tiles;
     // workgroups go to the 8 dies in turn: each die takes one run of items, so
@@ -260,50 +269,61 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     // are no routes; -1: outside; rows behind the tile's repeat its last).  Found while no product is pending: registers are free then, and the reads
     // wait for nothing but loads of the tile's own last steps.
     TileItem next_tile;
-    auto find_item = [&]() {
-        next_tile = item_at<BM, BN>(first, a.offsets, a.E, a.rows, n_tiles, next_item, end);
+    int found = 0;  // tables of source rows take turns
+    auto find_tile = [&](auto offset) {
+        next_tile = item_at<BM, BN>(first, offset, a.E, n_tiles, next_item, end);
         next_item += per_die;
+    };
+    auto find_rows = [&]() {
+        found ^= BM;
         for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
             int src = min(r, next_tile.n - 1);
             if (a.sorted_routes) {
                 const int route = a.sorted_routes[next_tile.row0 + src];
                 src = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
             }
-            source[r] = src;
+            source[found + r] = src;
         }
     };
-    auto start_item = [&]() {
+    auto find_item = [&]() {
+        find_tile([&](int e) { return a.offsets ? min(max(a.offsets[e], 0), a.rows) : e * a.rows; });
+        find_rows();
+    };
+    auto start_tile = [&]() {  // all but what goes by the source rows
         load_tile = next_tile;
         load_step = 0;
         const TileItem& t = load_tile;
         const bool on = t.n > 0;
         const int w_rows = on ? min(BN, a.N - t.n0) : 0;
         const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
+        w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
+        w_scale_base = a.w_scales + w0 * blocks;
+        ws_buf = buffer_of(w_scale_base, (uint32_t)(w_rows * blocks));
         const int64_t a0 = a.sorted_routes ? 0 : t.row0;
         const int64_t a_rows = !on ? 0 : a.sorted_routes ? a.a_rows : t.n;
         a_buf = buffer_of(a.a_codes + a0 * K2, (uint32_t)(a_rows * K2));
-        w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
         a_scale_base = a.a_scales + a0 * blocks;
         as_buf = buffer_of(a_scale_base, (uint32_t)(a_rows * blocks));
-        ws_buf = buffer_of(a.w_scales + w0 * blocks, (uint32_t)(w_rows * blocks));
-        w_scale_base = a.w_scales + w0 * blocks;
+    };
+    auto start_rows = [&]() {
+        const int w_rows = min(BN, a.N - load_tile.n0);
 #pragma unroll
         for (int j = 0; j < LOADS_A; ++j) {
-            const int row = source[(j * WAVES + wave) * 8 + (lane >> 3)];
+            const int row = source[found + (j * WAVES + wave) * 8 + (lane >> 3)];
             code_at[j] = row < 0 ? kOutside : row * (uint32_t)K2 + load_chunk;
         }
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
-            const int row = r0 < BM ? source[r0 + (lane >> 1)] : min(r0 - BM + (lane >> 1), w_rows - 1);
+            const int row = r0 < BM ? source[found + r0 + (lane >> 1)] : min(r0 - BM + (lane >> 1), w_rows - 1);
             scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + (lane & 1) * 16;
         }
     };
-    // codes of the loading side's step into stage `stage`
-    auto load_codes = [&](int stage) {
+    // codes of the loading side's step into stage `stage`; loads [from, to) of the wavefront
+    auto load_part = [&](int stage, auto from, auto to) {
         const uint32_t at = (uint32_t)load_step * kStepBytes;
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
+        for (int j = decltype(from)::value; j < decltype(to)::value; ++j) {
             uint32_t off = j < LOADS_A ? code_at[j < LOADS_A ? j : 0] : w_at + (uint32_t)((j - LOADS_A) * WAVES * 8) * K2;
             if constexpr (!WHOLE) {
                 if (at + load_chunk >= (uint32_t)K2) off = kOutside;
@@ -311,15 +331,19 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
         }
     };
+    constexpr std::integral_constant<int, 0> kFirst;
+    constexpr std::integral_constant<int, LOADS_A> kWeights;
+    constexpr std::integral_constant<int, LOADS> kEnd;
+    auto load_codes = [&](int stage) { load_part(stage, kFirst, kEnd); };
     u32x4 scale_regs[WHOLE ? 1 : SCALE_LOADS];
-    auto load_scales = [&]() {  // of the group that starts at the loading side's step
+    auto load_scales = [&](int buffer) {  // of the group that starts at the loading side's step
         const int at = load_step * 8;
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
             if (r0 >= ROWS) continue;
             if constexpr (WHOLE) {
-                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], at, scales + r0 * kScaleBytes);
+                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], at, scales + (buffer * ROWS + r0) * kScaleBytes);
             } else {
                 u32x4 v = {};
                 if (load_tile.n > 0 && scale_at[j] != kOutside) {
@@ -341,26 +365,33 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             }
         }
     };
-    auto store_scales = [&]() {  // the register path's second half
+    auto store_scales = [&](int buffer) {  // the register path's second half
         if constexpr (!WHOLE) {
 #pragma unroll
             for (int j = 0; j < SCALE_LOADS; ++j) {
                 const int r0 = (j * WAVES + wave) * 32;
                 if (r0 < ROWS) {
-                    *reinterpret_cast<u32x4*>(scales + (r0 + (lane >> 1)) * kScaleBytes + (lane & 1) * 16) = scale_regs[j];
+                    *reinterpret_cast<u32x4*>(scales + (buffer * ROWS + r0 + (lane >> 1)) * kScaleBytes + (lane & 1) * 16) = scale_regs[j];
                 }
             }
         }
     };
-    find_item();
+    find_tile([&](int e) { return max(scratch[e], 0); });
+    start_tile();
+    load_part(0, kWeights, kEnd);  // weights do not wait for the table of rows
+    find_rows();
     __syncthreads();
-    start_item();
-    __syncthreads();
-    find_item();
-    load_scales();
-    store_scales();
-    load_codes(0);
+    start_rows();
+    load_part(0, kFirst, kWeights);
+    load_scales(0);
+    store_scales(0);
     ++load_step;
+#pragma unroll
+    for (int i = 1; i < STAGES - 1; ++i) {
+        load_codes(i);
+        ++load_step;
+    }
+    find_item();
 
     // chunk 2 t + half of row c
     uint32_t read_at[4];
@@ -378,21 +409,22 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             x[t & 1][j] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ((wm * MT + j) * 32) * kStepBytes + read_at[t]);
         }
     };
-    auto read_scales = [&](int to, int step) {  // of one step of the group; byte 0 and 2 of a word are the lane's
+    auto read_scales = [&](int to, int buffer, int step) {  // of one step of the group; byte 0 and 2 of a word are the lane's
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            sw[to][i] = *reinterpret_cast<const u32x2*>(scales + (BM + (wn * NT + i) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+            sw[to][i] = *reinterpret_cast<const u32x2*>(scales + (buffer * ROWS + BM + (wn * NT + i) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            sa[to][j] = *reinterpret_cast<const u32x2*>(scales + ((wm * MT + j) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+            sa[to][j] = *reinterpret_cast<const u32x2*>(scales + (buffer * ROWS + (wm * MT + j) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
         }
     };
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    load_codes(1);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
+    load_codes(STAGES - 1);
     ++load_step;
-    read_scales(0, 0);
+    read_scales(0, 0, 0);
     read_codes(0, 0);
+    int buffer = 0;
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
         f32x16 acc[NT][MT];
@@ -422,27 +454,35 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                     __builtin_amdgcn_sched_barrier(0);
                 };
                 // reads stand before the products that they hide behind; unfenced they sink to their use
-                read_codes(s & 1, 1);
-                if (s == kGroupSteps - 1) store_scales();
+                constexpr int LAST = kGroupSteps - 1;
+                const int next_buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
+                read_codes(s % STAGES, 1);
+                if (s == LAST) store_scales(next_buffer);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 0>{});
-                read_codes(s & 1, 2);
-                if (s < kGroupSteps - 1) read_scales((s + 1) & 1, s + 1);
+                read_codes(s % STAGES, 2);
+                if (s < LAST) read_scales((s + 1) & 1, buffer, s + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 1>{});
-                read_codes(s & 1, 3);
+                read_codes(s % STAGES, 3);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 2>{});
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                read_codes((s + 1) & 1, 0);
-                if (s == kGroupSteps - 1) read_scales(0, 0);
+                // the next step has landed once no more than the loads behind it are left
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
+                read_codes((s + 1) % STAGES, 0);
+                if (s == LAST) read_scales(0, next_buffer, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                if (s == kGroupSteps - 2) load_scales();
-                load_codes(s & 1);
+                // the step loaded here is STAGES ahead: the first of a group brings the group's scales
+                if (s == kGroupSteps - STAGES) load_scales(next_buffer);
+                load_codes(s % STAGES);
                 multiply(std::integral_constant<int, 3>{});
                 ++load_step;
-                if (s == 1 && load_step == steps) start_item();  // a group ends a tile: its last step is loaded here
+                if ((s + STAGES) % kGroupSteps == LAST && load_step == steps) {  // tiles end with a group
+                    start_tile();
+                    start_rows();
+                }
             }
+            buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
         }
         find_item();
 #pragma unroll
@@ -466,7 +506,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 constexpr int kCUs = 256;
 
 // wgs_per_cu: as many as fit by LDS and registers.
-template <int DT, int MT, int NT, int WM, int WN>
+template <int DT, int MT, int NT, int WM, int WN, int STAGES>
 hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 {
     constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
@@ -477,18 +517,21 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
     if (grid > kCUs * wgs_per_cu) grid = kCUs * wgs_per_cu;
     const bool whole = a.K % 1024 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
-    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
-    else launch(tiled_kernel<DT, MT, NT, WM, WN, false>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
+    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
+    else launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
     return hipGetLastError();
 }
 
 // Tile by the mean rows of an expert that has some and by how many tiles that
-// makes; measured with E = 8, N = 4096, K = 2048 unless said otherwise, us:
-//   rows   8: 32x64   7.7, 64x128   8.9       rows  128: 32x64 10.6, 64x128 11.7
-//   rows 512: 64x128 13.5, 128x128 15.4       rows 1024: 64x128 22.0, 128x128 17.2
-//   rows 8192: 128x128 62.5, 256x256 72.4 (576 tiles of 256 x 256 for 256 CUs)
-//   rows 8192, K 4096, N 8192: 128x128 205, 256x256 188 (1152 tiles)
-//   rows 1024, E = 1, N = 2048: 64x128 8.7, 128x128 10.0 (too few tiles)
+// makes.  Measured in us, weights out of cache, K = 2048 unless said otherwise:
+//   E 8, N 4096:  rows    8: 32x64 8.2, 64x128 9.6;    rows  128: 10.6, 12.3
+//                 rows  512: 32x64 16.2, 64x128 14.1, 128x128 16.0
+//                 rows 1024: 64x128 22.8, 128x128 19.0
+//                 rows 8192: 128x128 62.5, 256x256 72.4 (576 tiles of 256 x 256)
+//   E 8, N 8192, K 4096, rows 8192: 128x128 205, 256x256 188 (1152 tiles)
+//   E 1, N 2048:  rows 1024: 64x128 8.7, 128x128 10.0 (too few tiles for the CUs)
+//   E 512, N 1536: rows  60: 32x64 with four stages 20.8, with two 25.0
+// The four-stage form loads up to a tile ahead, so K must make two groups.
 template <int DT>
 hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
 {
@@ -497,10 +540,13 @@ hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
     auto tiles = [&](int bm, int bn) {  // an expert's last tile counts half
         return (a.rows / bm + experts / 2 + 1) * ((a.N + bn - 1) / bn);
     };
-    if (mean <= 16) return launch_tiled<DT, 1, 1, 1, 2>(a, 5, s);
-    if (mean <= 64 || tiles(128, 128) < kCUs) return launch_tiled<DT, 1, 2, 2, 2>(a, 2, s);
-    if (tiles(256, 256) < 5 * kCUs / 2) return launch_tiled<DT, 2, 2, 2, 2>(a, 2, s);
-    return launch_tiled<DT, 2, 4, 4, 2>(a, 1, s);
+    if (mean <= 16) {
+        if (a.K <= 1024) return launch_tiled<DT, 1, 1, 1, 2, 2>(a, 4, s);
+        return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
+    }
+    if (mean <= 64 || tiles(128, 128) < kCUs) return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
+    if (tiles(256, 256) < 5 * kCUs / 2) return launch_tiled<DT, 2, 2, 2, 2, 2>(a, 2, s);
+    return launch_tiled<DT, 2, 4, 4, 2, 2>(a, 1, s);
 }
 
 }  // namespace

@@ -52,6 +52,8 @@ PERMUTE = [
     (2100, 33, 9, 8, F16, 0.1, False),    # 16,800 routes: counted in spans
     (20000, 8, 64, 1, F16, 0.0, True),    # spans of one-route tokens
     (3000, 16, 1000, 7, F32, 0.2, False),  # spans with many experts
+    (40000, 8, 5, 4, BF16, 0.1, False),   # few experts in spans
+    (70000, 4, 20, 3, F16, 0.05, False),  # more than 64 routes a workgroup
     (19, 8, 31, 1024, BF16, 0.2, False),  # spans of 1024-route tokens
 ]
 

@@ -212,6 +212,50 @@ def test_matmul_dense_row_counts(rows, K):
     _matmul_case(rows, 1, 1, K, 272, BF16, False, rows + K)
 
 
+# E, K, N, rows of each expert, gather, dtype: enough tiles for the largest tile shape, K with and
+# without whole groups of 1024, partial tiles on both sides, rows behind the last expert
+LARGE = [
+    (1, 1024, 16384, [2560], False, F32),
+    (3, 1024, 16400, [1, 2047, 600], True, BF16),
+    (3, 96, 16390, [256, 0, 2400], False, F16),
+    (2, 2048, 10000, [3000, 1100], True, F16),
+    (2, 1312, 9001, [4097, 255], False, F32),
+    (4, 5120, 12288, [700, 900, 20, 1800], True, BF16),
+]
+
+
+@pytest.mark.parametrize("E,K,N,counts,gather,dtype", LARGE)
+def test_matmul_large(E, K, N, counts, gather, dtype):
+    g = torch.Generator(device="cuda").manual_seed(K + N)
+
+    def operand(*shape):
+        codes = torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=g, device="cuda").to(torch.uint8)
+        scales = torch.randint(115, 125, (*shape[:-1], shape[-1] // 32), generator=g, device="cuda").to(torch.uint8)
+        return codes, scales
+
+    rows = sum(counts) + 70
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    k = 2 if gather else 1
+    a, w = operand(-(-rows // k), K), operand(E, N, K)
+    routes = torch.randperm(rows, generator=g, device="cuda").int() if gather else None
+    out = qm.mx_matmul(*a, *w, off, sorted_routes=routes, top_k=k, dtype=dtype)
+    assert int(out[sum(counts):].count_nonzero()) == 0
+    av = qm.mx_dequantize(*a, F32).double()
+    av = av[routes.long() // k] if gather else av
+    o = off.tolist()
+    for e in range(E):
+        if o[e] == o[e + 1]:
+            continue
+        wt = qm.mx_dequantize(w[0][e], w[1][e], F32).double().T.contiguous()
+        want, mag = av[o[e]:o[e + 1]] @ wt, av[o[e]:o[e + 1]].abs() @ wt.abs()
+        acc = K * 2 * ref.U32 * mag
+        tol = acc + ref.HALF_STEP[dtype] * (want.abs() + acc) + ref.HALF_MIN[dtype]
+        assert bool(((out[o[e]:o[e + 1]].double() - want).abs() <= tol).all())
+    for _ in range(3):  # every launch gives the same bits
+        again = qm.mx_matmul(*a, *w, off, sorted_routes=routes, top_k=k, dtype=dtype)
+        assert torch.equal(again, out)
+
+
 def test_matmul_scale_range():
     # products of scales far from 1: 2^-120 .. 2^120 in float32
     for lo, hi in ((60, 80), (172, 184), (0, 120), (100, 155)):
