@@ -436,68 +436,66 @@ def _row_dtype(dt: torch.dtype, name: str) -> int:
     return code
 
 
-def _device(t, name: str, dim: int) -> torch.device:
-    """The device of a call's leading tensor, which must have `dim` dimensions."""
+def _index(t, name: str, dim: int) -> int:
+    """The device index of a call's leading tensor, which must have `dim` dimensions."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    return t.device
+    return t.get_device()
 
 
-def _tensor(t, name: str, device, dtype, shape) -> int:
-    """Checks a contiguous tensor on `device`; its address."""
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype is dtype and t.shape == shape
+def _tensor(t, name: str, index: int, dtype, shape) -> int:
+    """Checks a contiguous tensor on device `index`; its address."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
             and t.is_contiguous()):
         _dev(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     return t.data_ptr()
 
 
-def _rows(t, name: str, device, n: int) -> int:
+def _rows(t, name: str, index: int, n: int) -> int:
     """Checks a matrix of n rows (any row stride, neighbouring elements); its row stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dim() != 2 or t.shape[0] != n:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {n} rows")
     h = t.shape[1]
     if h < 1:
         raise ValueError(f"{name} has no columns")
-    if n <= 1:
-        if h > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
+    if t.is_contiguous():
         return h
     stride, step = t.stride()
-    if h > 1 and step != 1 or stride < h:
+    if h > 1 and step != 1 or n > 1 and stride < h:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
-    return stride
+    return stride if n > 1 else h
 
 
-def _elsewhere(device, stream) -> bool:
+def _elsewhere(index: int, stream) -> bool:
     """Whether a call must be made under _on(): on a given stream or not on the current device."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or index != torch.cuda.current_device()
 
 
-def _on(device, stream):
+def _on(index: int, stream):
     """Makes the device and the stream current, so that outputs are allocated for the stream that
     fills them and the launch goes to the tensors' device."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+        stream = torch.cuda.current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{index}")
     return torch.cuda.stream(stream)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(device) -> int:
+def _current(index: int) -> int:
     """The handle of the current stream (without the Stream object, which costs microseconds)."""
     if _raw_stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _raw_stream(device.index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return _raw_stream(index)
 
 
 def permute_workspace_size(T: int, top_k: int, E: int) -> int:
@@ -512,7 +510,7 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
     hidden: float16, bfloat16 or float32 [T, H], any row stride; None: rows is None and only the
     maps are made.  Ids outside [0, E) drop their route: its row, behind the last expert's, is zero
     and its route_rows entry is -1 - row."""
-    dev = _device(topk_ids, "topk_ids", 2)
+    dev = _index(topk_ids, "topk_ids", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return permute(hidden, topk_ids, E, workspace=workspace)
@@ -528,7 +526,7 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
     if workspace is not None:
         _tensor(workspace, "workspace", dev, torch.uint8, workspace.shape)
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = topk_ids.new_empty((need,), dtype=torch.uint8)
     offsets = topk_ids.new_empty((max(E, 0) + 1,))
     order = topk_ids.new_empty((R,))
     route_rows = torch.empty_like(topk_ids)
@@ -542,7 +540,7 @@ def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[to
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows back to their tokens: out[t] = sum over slots of weights[t, s] * rows[route_rows[t, s]]
     (float32 sums, rounded once; no weights: 1); dropped routes add nothing."""
-    dev = _device(route_rows, "route_rows", 2)
+    dev = _index(route_rows, "route_rows", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return unpermute(rows, route_rows, weights, out=out)
@@ -569,7 +567,7 @@ def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], rou
                        weights: Optional[torch.Tensor] = None, *, stream=None):
     """The gradient of unpermute: (grad_rows [T*k, H], grad_weights float32 [T, k]).  rows None:
     grad_weights is not computed (None), as for an unpermute without weights."""
-    dev = _device(route_rows, "route_rows", 2)
+    dev = _index(route_rows, "route_rows", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return unpermute_backward(grad_out, rows, route_rows, weights)
@@ -584,7 +582,7 @@ def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], rou
         if rows.dtype is not grad_out.dtype or rows.shape[1] != H:
             raise ValueError(f"rows is {rows.dtype} {tuple(rows.shape)}, expected {grad_out.dtype} "
                              f"{(T * top_k, H)}")
-        grad_weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        grad_weights = route_rows.new_empty(shape, dtype=torch.float32)
     w = None if weights is None else _tensor(weights, "weights", dev, torch.float32, shape)
     grad_rows = grad_out.new_empty((T * top_k, H))
     _check(load_library().qmoe_unpermute_backward(
@@ -599,7 +597,7 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
     its rows, giving codes [E, K, rows/2] and scales [E, K, rows/32] of the transposed matrices."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA (HIP) tensor")
-    dev = x.device
+    dev = x.get_device()
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return mx_quantize(x, transpose=transpose)
@@ -610,8 +608,8 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
             raise ValueError("x must have 2 or 3 dimensions to be quantised along its rows")
         _dev(x, "x")
         *lead, rows, K = x.shape
-        codes = torch.empty((*lead, K, rows // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((*lead, K, rows // MX_BLOCK), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((*lead, K, rows // 2), dtype=torch.uint8)
+        scales = x.new_empty((*lead, K, rows // MX_BLOCK), dtype=torch.uint8)
         _check(lib.qmoe_mx_quantize_columns(x.data_ptr(), lead[0] if lead else 1, rows, K, dt,
                                             codes.data_ptr(), scales.data_ptr(), _current(dev)))
         return codes, scales
@@ -624,26 +622,27 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
     else:
         _dev(x, "x")
         rows, stride = math.prod(lead), K
-    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((*lead, K // MX_BLOCK), dtype=torch.uint8, device=dev)
+    codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
+    scales = x.new_empty((*lead, K // MX_BLOCK), dtype=torch.uint8)
     _check(lib.qmoe_mx_quantize(x.data_ptr(), stride, rows, K, dt, codes.data_ptr(), scales.data_ptr(),
                                 _current(dev)))
     return codes, scales
 
 
-def _mx(codes, scales, name: str, device) -> int:
+def _mx(codes, scales, name: str, index: int) -> int:
     """Checks a pair of codes [..., K/2] and scales [..., K/32]; K."""
-    if not isinstance(codes, torch.Tensor):
-        raise ValueError(f"{name}_codes must be a CUDA (HIP) tensor")
-    shape = codes.shape
-    if len(shape) < 1:
-        raise ValueError(f"{name}_codes must have at least 1 dimension")
-    _tensor(codes, f"{name}_codes", device, torch.uint8, shape)
-    K = shape[-1] * 2
-    if K % MX_BLOCK:
-        raise ValueError(f"{name}_codes holds {K} values a row, which are no whole blocks of {MX_BLOCK}")
-    _tensor(scales, f"{name}_scales", device, torch.uint8, (*shape[:-1], K // MX_BLOCK))
-    return K
+    if (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.get_device() == index
+            and scales.get_device() == index and codes.dtype is torch.uint8 and scales.dtype is torch.uint8
+            and codes.is_contiguous() and scales.is_contiguous()):
+        *lead, half = codes.shape or (0,)
+        if half % 16 == 0 and scales.shape == (*lead, half // 16):
+            return half * 2
+    _dev(codes, f"{name}_codes", torch.uint8)
+    _dev(scales, f"{name}_scales", torch.uint8)
+    if codes.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{name}_codes is on {codes.device}, {name}_scales on {scales.device}, expected cuda:{index}")
+    raise ValueError(f"{name}_codes {tuple(codes.shape)} (two values a byte) and {name}_scales "
+                     f"{tuple(scales.shape)} (one byte for {MX_BLOCK} values) do not belong together")
 
 
 def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype, *,
@@ -652,14 +651,14 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
     dt = _row_dtype(dtype, "dtype")
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
         raise ValueError("codes must be a CUDA (HIP) tensor")
-    dev = codes.device
+    dev = codes.get_device()
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return mx_dequantize(codes, scales, dtype, out=out)
     K = _mx(codes, scales, "mx", dev)
     shape = (*codes.shape[:-1], K)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = codes.new_empty(shape, dtype=dtype)
     to = _tensor(out, "out", dev, dtype, shape)
     _check(load_library().qmoe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), math.prod(shape[:-1]), K, dt,
                                              to, _current(dev)))
@@ -678,7 +677,7 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     a's row sorted_routes[r] // top_k; without it row r takes a's row r.  Rows behind the last
     expert's are zero."""
     dt = _row_dtype(dtype, "dtype")
-    dev = _device(a_codes, "a_codes", 2)
+    dev = _index(a_codes, "a_codes", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return mx_matmul(a_codes, a_scales, w_codes, w_scales, expert_offsets, sorted_routes=sorted_routes,
@@ -694,11 +693,11 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
         offsets = _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
     A = rows = a_codes.shape[0]
     if sorted_routes is not None:
-        _device(sorted_routes, "sorted_routes", 1)
+        _index(sorted_routes, "sorted_routes", 1)
         rows = sorted_routes.shape[0]
         routes = _tensor(sorted_routes, "sorted_routes", dev, torch.int32, (rows,))
     if out is None:
-        out = torch.empty((rows, N), dtype=dtype, device=dev)
+        out = a_codes.new_empty((rows, N), dtype=dtype)
     to = _tensor(out, "out", dev, dtype, (rows, N))
     _check(load_library().qmoe_mx_matmul(
         a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
