@@ -13,9 +13,10 @@
 //
 // Counting.  Up to kOneLaunchRoutes routes every workgroup counts all of them
 // itself (ids come from L2), so the whole operator is one launch; above it,
-// count_kernel counts spans of about kSpanRoutes routes, scan_kernel turns
-// the counts into each span's start per expert, and a workgroup counts only
-// the part of its span before its own tokens.
+// count_kernel counts spans of about kSpanRoutes routes first, and a workgroup
+// adds up the spans before its own and counts the part of its span before its
+// tokens.  From more than kSummedSpans spans on, scan_kernel adds them up for
+// everybody.
 //
 // Back.  out[t] = sum over slots, in slot order, of w[t, s] * rows[row(t, s)]
 // in float32, rounded once; the gradient of the sort is the same sum without
@@ -36,7 +37,8 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 1024;
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int64_t kOneLaunchRoutes = 16384;
+constexpr int64_t kOneLaunchRoutes = 8192;
+constexpr int kSummedSpans = 32;
 constexpr int kSpanRoutes = 4096;  // (a span is at most that or one workgroup's tokens)
 
 __device__ inline int route_key(int id, int E) { return id >= 0 && id < E ? id : E; }
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
     const void* __restrict__ hidden, int64_t row_stride, int64_t T, int H,
     const int32_t* __restrict__ ids, int top_k, int E, void* __restrict__ rows,
     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted, int32_t* __restrict__ route_rows,
-    const int32_t* __restrict__ span_starts, const int32_t* __restrict__ totals, SortShape sh)
+    const int32_t* __restrict__ counts, int summed, const int32_t* __restrict__ totals, SortShape sh)
 {
     typedef typename std::conditional<EB == 2, uint16_t, uint32_t>::type Raw;
     __shared__ int before[kMaxExperts + 1];  // routes of the key before this workgroup's, then its next row
@@ -175,8 +177,19 @@ __global__ __launch_bounds__(kSortThreads) void permute_kernel(
     }
 
     for (int e = tid; e <= E; e += kSortThreads) {
-        before[e] = spans ? span_starts[span * (E + 1) + e] : 0;
-        base[e] = spans ? totals[e] : 0;
+        int b = 0, all = 0;
+        if (spans && totals) {  // counts[span] was made the count in earlier spans
+            b = counts[span * (E + 1) + e];
+            all = totals[e];
+        } else if (spans) {
+            for (int c = 0; c < summed; ++c) {
+                const int n = counts[c * (E + 1) + e];
+                if (c < span) b += n;
+                all += n;
+            }
+        }
+        before[e] = b;
+        base[e] = all;
     }
     __syncthreads();
     {
@@ -460,27 +473,27 @@ int64_t permute_ws_ints(int64_t T, int top_k, int E)
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s)
 {
     const SortShape sh = sort_shape(a.T, a.top_k);
-    const int32_t* starts = nullptr;
     const int32_t* totals = nullptr;
-    if (sh.wgs_per_span) {
-        const int64_t spans = span_count(a.T, sh);
-        int32_t* tot = a.ws + spans * (a.E + 1);
+    const int64_t spans = sh.wgs_per_span ? span_count(a.T, sh) : 0;
+    if (spans > 0) {
         launch(count_kernel, dim3((unsigned)spans), dim3(kSortThreads), s, a.ids, a.T * a.top_k, a.E,
                sh.tokens_per_wg * sh.wgs_per_span * a.top_k, a.ws);
-        hipError_t e = hipGetLastError();
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
+    }
+    if (spans > kSummedSpans) {
+        int32_t* tot = a.ws + spans * (a.E + 1);
         launch(scan_kernel, dim3((unsigned)((a.E + 1 + 63) / 64)), dim3(64 * kScanParts), s, a.ws, (int)spans,
                a.E + 1, tot);
-        e = hipGetLastError();
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        starts = a.ws;
         totals = tot;
     }
     // T = 0 still launches one workgroup, which writes the offsets
     const int64_t wgs = a.T > 0 ? (a.T + sh.tokens_per_wg - 1) / sh.tokens_per_wg : 1;
     auto go = [&](auto kernel) {
         launch(kernel, dim3((unsigned)wgs), dim3(kSortThreads), s, a.hidden, a.row_stride, a.T, a.H, a.ids,
-               a.top_k, a.E, a.rows, a.offsets, a.sorted_routes, a.route_rows, starts, totals, sh);
+               a.top_k, a.E, a.rows, a.offsets, a.sorted_routes, a.route_rows, (const int32_t*)a.ws, (int)spans, totals, sh);
     };
     if (a.elem == 2) {
         if (a.H >= 8) go(permute_kernel<2, 8>);
