@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 
     const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % WM, wn = wave / WM;
+    const int wm = wave / WN, wn = wave % WN;
     const int K2 = a.K / 2, blocks = a.K / 32;
     const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps;  // whole groups
 
@@ -427,6 +427,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     int buffer = 0;
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
+        // wavefronts whose rows lie behind the tile's leave their products out; the two wavefronts of
+        // a SIMD hold different row blocks, so a half-full tile takes half the time
+        const bool active = wm * MT * 32 < tile.n;
         f32x16 acc[NT][MT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -438,7 +441,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             for (int s = 0; s < kGroupSteps; ++s) {
                 auto multiply = [&](auto quarter) {
                     constexpr int t = decltype(quarter)::value;
-                    if (!WHOLE && (g + s) * 256 + t * 64 >= a.K) return;
+                    if (!active || (!WHOLE && (g + s) * 256 + t * 64 >= a.K)) return;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
 #pragma unroll
