@@ -421,7 +421,7 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
                        int32_t dtype, void* out, void* stream);
 
 /*
- * Grouped product of MXFP4 rows with MXFP4 expert weights:
+ * Grouped product of MXFP4 rows with MXFP4 expert weights, one launch:
  *   out[r, n] = sum_k a[src(r), k] * w[e(r), n, k]
  * accumulated in float32 by the scaled matrix instruction, rounded once.
  *   a_codes, a_scales  [a_rows, K/2], [a_rows, K/32]
@@ -436,7 +436,8 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *                      outside [0, a_rows) stands for a row of zeros
  *   top_k              >= 1, used with sorted_routes
  *   out                dtype [rows, N] out (F16, BF16 or F32)
- * Scales of 255 (NaN) make the outputs they enter NaN.  Requires 1 <= E <=
+ * Scales of 255 (NaN) make the outputs they enter NaN.  expert_offsets must not
+ * change while the call runs.  Requires 1 <= E <=
  * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24, and with
  * sorted_routes a_rows * K/2 < 2^31 (else QMOE_ERR_UNSUPPORTED).  rows = 0
  * returns QMOE_OK and enqueues nothing.

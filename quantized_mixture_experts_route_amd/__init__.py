@@ -424,8 +424,10 @@ def raw_codes(proj: Projection, E: int, N: int, K: int, block_size: int, dtype: 
 
 
 # ------------------------------------------------ sorted by expert and back, MXFP4
-# One call of these takes a few microseconds on the GPU, so the binding's own time counts: a tensor
-# that is right passes one comparison, and the message is worked out only for one that is not.
+# None of these is recorded by autograd: the gradients are calls of their own (permute_backward,
+# unpermute_backward, mx_matmul on weights quantised with transpose=True).  One call takes a few
+# microseconds on the GPU, so the binding's own time counts: a tensor that is right passes one
+# comparison, and the message is worked out only for one that is not.
 _ROW_DTYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
 

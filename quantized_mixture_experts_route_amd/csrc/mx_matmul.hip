@@ -56,12 +56,13 @@ __device__ inline i32x8 operand(u32x4 v)
 // scales go through registers, byte by byte at the end of a row, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 600 us, 3.2
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 575 us, 3.35
 // PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
 // instructions alone would take 354 us (power holds them at 1.8 GHz), loads
-// alone 360 us (64 KB a step and CU from L2, 12 TB/s), storing 470 MB 100 us.
-// 8192^3, one expert: 270 us, 4.1 PFLOP/s.  Few rows: HBM; 60 rows over 512
-// experts 20.9 us for 96 MB (4.6 TB/s).
+// alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
+// storing 470 MB adds 100 us: the three overlap in part only, since one
+// workgroup fills a CU.  8192^3, one expert: 274 us, 4.0 PFLOP/s.  Few rows:
+// HBM; 60 rows over 512 experts 20.9 us for 96 MB (4.6 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row
@@ -250,12 +251,17 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     // rows behind the last expert's are zero
     if (a.offsets) {
         const int64_t lo = (int64_t)min(max(a.offsets[a.E], 0), a.rows) * a.N, hi = (int64_t)a.rows * a.N;
-        for (int64_t i = lo + blockIdx.x * THREADS + threadIdx.x; i < hi; i += (int64_t)gridDim.x * THREADS) {
-            ((Raw*)a.out)[i] = RowType<DT>::round(0.0f);
+        constexpr int V = 16 / sizeof(Raw);
+        for (int64_t i = lo + (blockIdx.x * (int64_t)THREADS + threadIdx.x) * V; i < hi; i += (int64_t)gridDim.x * THREADS * V) {
+            if (i + V <= hi) {
+                store_vec<Raw, V>((Raw*)a.out + i, RowVec<Raw, V>{});
+            } else {
+                for (int64_t q = i; q < hi; ++q) ((Raw*)a.out)[q] = 0;
+            }
         }
     }
 
-    // ---- the loading side: an item and a step, up to two steps ahead
+    // ---- the loading side: an item and a step, up to STAGES steps ahead
     TileItem load_tile;
     int load_step = 0;
     const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
@@ -266,8 +272,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const uint8_t *a_scale_base = nullptr, *w_scale_base = nullptr;
 
     // The next item, and in LDS its rows' source rows in a (from the tile's first row where there
-    // are no routes; -1: outside; rows behind the tile's repeat its last).  Found while no product is pending: registers are free then, and the reads
-    // wait for nothing but loads of the tile's own last steps.
+    // are no routes; -1: outside; rows behind the tile's repeat its last).  Found while no product is
+    // pending: registers are free then, and the reads wait for nothing but loads of the last steps.
     TileItem next_tile;
     int found = 0;  // tables of source rows take turns
     auto find_tile = [&](auto offset) {
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             }
         }
     };
-    find_tile([&](int e) { return max(scratch[e], 0); });
+    find_tile([&](int e) { return scratch[e]; });
     start_tile();
     load_part(0, kWeights, kEnd);  // weights do not wait for the table of rows
     find_rows();
