@@ -10,6 +10,7 @@ PyTorch provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -477,7 +478,7 @@ def _rows(t, name: str, index: int, n: int) -> int:
 
 def _elsewhere(index: int, stream) -> bool:
     """Whether a call must be made under _on(): on a given stream or not on the current device."""
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != _current_device()
 
 
 def _on(index: int, stream):
@@ -490,16 +491,19 @@ def _on(index: int, stream):
     return torch.cuda.stream(stream)
 
 
+# what torch.cuda's own functions call, without the objects and checks around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current(index: int) -> int:
-    """The handle of the current stream (without the Stream object, which costs microseconds)."""
+    """The handle of the current stream."""
     if _raw_stream is None:
         return torch.cuda.current_stream(index).cuda_stream
     return _raw_stream(index)
 
 
+@functools.lru_cache(maxsize=256)
 def permute_workspace_size(T: int, top_k: int, E: int) -> int:
     return int(load_library().qmoe_permute_workspace_size(T, top_k, E))
 
@@ -524,7 +528,7 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
         stride, H, dt = _rows(hidden, "hidden", dev, T), hidden.shape[1], _row_dtype(hidden.dtype, "hidden")
         rows = hidden.new_empty((R, H))
     lib = load_library()
-    need = lib.qmoe_permute_workspace_size(T, top_k, E)
+    need = permute_workspace_size(T, top_k, E)
     if workspace is not None:
         _tensor(workspace, "workspace", dev, torch.uint8, workspace.shape)
     elif need:
@@ -554,7 +558,9 @@ def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[to
     w = None if weights is None else _tensor(weights, "weights", dev, torch.float32, shape)
     if out is None:
         out = rows.new_empty((T, H))
-    to = _tensor(out, "out", dev, rows.dtype, (T, H))
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, rows.dtype, (T, H))
     _check(load_library().qmoe_unpermute(rows.data_ptr(), stride, at, w, T, top_k, H, dt, to, _current(dev)))
     return out
 
@@ -661,7 +667,9 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
     shape = (*codes.shape[:-1], K)
     if out is None:
         out = codes.new_empty(shape, dtype=dtype)
-    to = _tensor(out, "out", dev, dtype, shape)
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, dtype, shape)
     _check(load_library().qmoe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), math.prod(shape[:-1]), K, dt,
                                              to, _current(dev)))
     return out
@@ -700,7 +708,9 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
         routes = _tensor(sorted_routes, "sorted_routes", dev, torch.int32, (rows,))
     if out is None:
         out = a_codes.new_empty((rows, N), dtype=dtype)
-    to = _tensor(out, "out", dev, dtype, (rows, N))
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, dtype, (rows, N))
     _check(load_library().qmoe_mx_matmul(
         a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
         routes, top_k, rows, dt, to, _current(dev)))
