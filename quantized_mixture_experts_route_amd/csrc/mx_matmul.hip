@@ -53,7 +53,7 @@ __device__ inline i32x8 operand(u32x4 v)
 //
 // WHOLE: K is a multiple of 1024 and the scale rows are 16-byte aligned, so
 // scales take the direct path to LDS too and no step has a tail.  Otherwise
-// scales go through registers, byte by byte at the end of a row, and codes
+// scales go through registers, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
 //
 // What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 575 us, 3.35
@@ -148,6 +148,36 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
         store(lane & 15, col, v[0]);
         store(16 + (lane & 15), col, v[1]);
     }
+}
+
+// The 16 scale bytes at p, `chunk` bytes into a row that has `left` more from
+// there: 0 behind the row's end, and nothing read outside the row.
+__device__ inline u32x4 load_scale_chunk(const uint8_t* p, int chunk, int left)
+{
+    uint64_t lo = 0, hi = 0;
+    if (left >= 16) {
+        __builtin_memcpy(&lo, p, 8);
+        __builtin_memcpy(&hi, p + 8, 8);
+    } else if (left > 0 && chunk > 0) {  // the row's last 16 bytes, shifted down
+        __builtin_memcpy(&lo, p + left - 16, 8);
+        __builtin_memcpy(&hi, p + left - 8, 8);
+        const int shift = 8 * (16 - left);
+        lo = shift < 64 ? lo >> shift | hi << (64 - shift) : hi >> (shift - 64);
+        hi = shift < 64 ? hi >> shift : 0;
+    } else if (left > 0) {  // a row of fewer than 16: one load for each bit of its length
+        uint64_t v8 = 0;
+        uint32_t v4 = 0;
+        uint16_t v2 = 0;
+        uint8_t v1 = 0;
+        if (left & 8) __builtin_memcpy(&v8, p, 8);
+        if (left & 4) __builtin_memcpy(&v4, p + (left & 8), 4);
+        if (left & 2) __builtin_memcpy(&v2, p + (left & 12), 2);
+        if (left & 1) v1 = p[left - 1];
+        const uint64_t rest = (uint64_t)v4 | (uint64_t)v2 << (8 * (left & 4)) | (uint64_t)v1 << (8 * (left & 6));
+        lo = left & 8 ? v8 : rest;
+        hi = left & 8 ? rest : 0;
+    }
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
@@ -353,19 +383,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             } else {
                 u32x4 v = {};
                 if (load_tile.n > 0 && scale_at[j] != kOutside) {
-                    const uint8_t* p = (r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at;
-                    const int left = blocks - at - (lane & 1) * 16;
-                    if (left >= 16) {
-                        __builtin_memcpy(&v, p, 16);
-                    } else {
-                        uint64_t part[2] = {};
-#pragma unroll 1
-                        for (int i = 0; i < left; ++i) {
-                            const uint64_t b = (uint64_t)p[i] << (8 * (i & 7));
-                            if (i < 8) part[0] |= b; else part[1] |= b;
-                        }
-                        __builtin_memcpy(&v, part, 16);
-                    }
+                    const int chunk = at + (lane & 1) * 16;
+                    v = load_scale_chunk((r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at, chunk, blocks - chunk);
                 }
                 scale_regs[j] = v;
             }
@@ -540,6 +559,7 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 //   E 8, N 8192, K 4096, rows 8192: 128x128 205, 256x256 188 (1152 tiles)
 //   E 1, N 2048:  rows 1024: 64x128 8.7, 128x128 10.0 (too few tiles for the CUs)
 //   E 512, N 1536: rows  60: 32x64 with four stages 20.8, with two 25.0
+//   E 512, N 2048, K 768: rows 512: 32x64 with two stages 50.3, 64x128 49.1
 // The four-stage form loads up to a tile ahead, so K must make two groups.
 template <int DT>
 hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
@@ -549,10 +569,7 @@ hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
     auto tiles = [&](int bm, int bn) {  // an expert's last tile counts half
         return (a.rows / bm + experts / 2 + 1) * ((a.N + bn - 1) / bn);
     };
-    if (mean <= 16) {
-        if (a.K <= 1024) return launch_tiled<DT, 1, 1, 1, 2, 2>(a, 4, s);
-        return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
-    }
+    if (mean <= 16 && a.K > 1024) return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
     if (mean <= 64 || tiles(128, 128) < kCUs) return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
     if (tiles(256, 256) < 5 * kCUs / 2) return launch_tiled<DT, 2, 2, 2, 2, 2>(a, 2, s);
     return launch_tiled<DT, 2, 4, 4, 2, 2>(a, 1, s);
