@@ -50,6 +50,7 @@ __device__ inline i32x8 operand(u32x4 v)
 //
 // LDS rows are 128 bytes (32 banks); the 16-byte chunk of row r sits in slot
 // chunk ^ (r / 2 % 8), so that 16 rows read at one chunk cover all 64 banks.
+// Scale rows of 32 bytes swap their halves where r / 8 is odd.
 //
 // WHOLE: K is a multiple of 1024 and the scale rows are 16-byte aligned, so
 // scales take the direct path to LDS too and no step has a tail.  Otherwise
@@ -297,7 +298,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
     uint32_t code_at[LOADS_A];      // byte offset of the lane's chunk at step 0
     const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk;  // rows behind N: out of bounds
-    uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's scale row
+    uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's half of a scale row's group
+    const uint32_t scale_chunk = ((lane & 1) ^ ((lane >> 4) & 1)) * 16;
     __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
     const uint8_t *a_scale_base = nullptr, *w_scale_base = nullptr;
 
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
             const int row = r0 < BM ? source[found + r0 + (lane >> 1)] : min(r0 - BM + (lane >> 1), w_rows - 1);
-            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + (lane & 1) * 16;
+            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + scale_chunk;
         }
     };
     // codes of the loading side's step into stage `stage`; loads [from, to) of the wavefront
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             } else {
                 u32x4 v = {};
                 if (load_tile.n > 0 && scale_at[j] != kOutside) {
-                    const int chunk = at + (lane & 1) * 16;
+                    const int chunk = at + scale_chunk;
                     v = load_scale_chunk((r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at, chunk, blocks - chunk);
                 }
                 scale_regs[j] = v;
@@ -434,14 +436,17 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             x[t & 1][j] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ((wm * MT + j) * 32) * kStepBytes + read_at[t]);
         }
     };
-    auto read_scales = [&](int to, int buffer, int step) {  // of one step of the group; byte 0 and 2 of a word are the lane's
+    // scale bytes of one step of the group; byte 0 and 2 of a word are the lane's
+    const uint32_t scales_at = c * kScaleBytes + ((c >> 3) & 1) * 16;
+    auto read_scales = [&](int to, int buffer, int step) {
+        const uint8_t* from = scales + buffer * ROWS * kScaleBytes + (scales_at ^ (step / 2 * 16)) + step % 2 * 8;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            sw[to][i] = *reinterpret_cast<const u32x2*>(scales + (buffer * ROWS + BM + (wn * NT + i) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+            sw[to][i] = *reinterpret_cast<const u32x2*>(from + (BM + (wn * NT + i) * 32) * kScaleBytes) >> (8 * half);
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            sa[to][j] = *reinterpret_cast<const u32x2*>(scales + (buffer * ROWS + (wm * MT + j) * 32 + c) * kScaleBytes + step * 8) >> (8 * half);
+            sa[to][j] = *reinterpret_cast<const u32x2*>(from + ((wm * MT + j) * 32) * kScaleBytes) >> (8 * half);
         }
     };
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
