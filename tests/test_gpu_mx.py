@@ -220,6 +220,7 @@ LARGE = [
     (3, 96, 16390, [256, 0, 2400], False, F16),
     (2, 2048, 10000, [3000, 1100], True, F16),
     (2, 1312, 9001, [4097, 255], False, F32),
+    (2, 96, 16390, [2000, 2400], True, F16),
     (4, 5120, 12288, [700, 900, 20, 1800], True, BF16),
 ]
 
