@@ -57,13 +57,14 @@ __device__ inline i32x8 operand(u32x4 v)
 // scales go through registers, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 575 us, 3.35
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 581 us, 3.3
 // PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
 // instructions alone would take 354 us (power holds them at 1.8 GHz), loads
 // alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
 // storing 470 MB adds 100 us: the three overlap in part only, since one
-// workgroup fills a CU.  8192^3, one expert: 274 us, 4.0 PFLOP/s.  Few rows:
-// HBM; 60 rows over 512 experts 20.9 us for 96 MB (4.6 TB/s).
+// workgroup fills a CU.  8192^3, one expert: 275 us, 4.0 PFLOP/s.  Rows that
+// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 440 us, K =
+// 4096 339.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row
