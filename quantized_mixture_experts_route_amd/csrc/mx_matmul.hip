@@ -63,7 +63,7 @@ __device__ inline i32x8 operand(u32x4 v)
 // alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
 // storing 470 MB adds 100 us: the three overlap in part only, since one
 // workgroup fills a CU.  8192^3, one expert: 275 us, 4.0 PFLOP/s.  Rows that
-// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 440 us, K =
+// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 412 us, K =
 // 4096 339.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
@@ -147,6 +147,27 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
             v[1][i] = t[1];
         }
         const int col = 8 * half + 16 * ((lane >> 4) & 1);
+        if (WHOLE && (((uintptr_t)out | (uintptr_t)N << 1) & 2)) {
+            // rows that start between two words: they are stored one column on, in whole words, with
+            // the first column of the neighbour's eight at the end; columns 0 and 31 on their own
+            // (18498 rows of 2175 columns: 90 us, with 16-byte stores that split words 105)
+            const int neighbour = lane < 32 ? lane + 32 : lane - 16;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                Raw* p = out + (int64_t)(16 * q + (lane & 15)) * N + col;
+                const uint32_t next = (uint32_t)__shfl((int)v[q][0], neighbour, kWave);
+                const bool odd = (uintptr_t)p & 2;
+                if (odd) {
+                    if (col == 0) p[0] = (Raw)v[q][0];
+                    if (col == 24) p[7] = (Raw)(v[q][3] >> 16);
+                    v[q] = u32x4{v[q][0] >> 16 | v[q][1] << 16, v[q][1] >> 16 | v[q][2] << 16,
+                                 v[q][2] >> 16 | v[q][3] << 16, v[q][3] >> 16 | next << 16};
+                }
+                __builtin_memcpy(p + odd, &v[q], 12);
+                if (!odd || col < 24) __builtin_memcpy(p + odd + 6, (const char*)&v[q] + 12, 4);
+            }
+            return;
+        }
         store(lane & 15, col, v[0]);
         store(16 + (lane & 15), col, v[1]);
     }
@@ -425,16 +446,20 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     uint32_t read_at[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) read_at[t] = c * (uint32_t)kStepBytes + (((2 * t + half) ^ ((c >> 1) & 7)) * 16);
-    u32x4 w[2][NT], x[2][MT];
+    // Operands of two quarters.  The largest tile with scales through registers has no room for them:
+    // spilled registers wait for the loads in flight, so there a quarter's operands are read right
+    // before it (8192 x 16384 x 4064: 456 -> 412 us).
+    constexpr bool AHEAD = WHOLE || MT * NT < 8;
+    u32x4 w[AHEAD ? 2 : 1][NT], x[AHEAD ? 2 : 1][MT];
     u32x2 sw[2][NT], sa[2][MT];
     auto read_codes = [&](int stage, int t) {  // operands of quarter t
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            w[t & 1][i] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + (BM + (wn * NT + i) * 32) * kStepBytes + read_at[t]);
+            w[AHEAD ? t & 1 : 0][i] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + (BM + (wn * NT + i) * 32) * kStepBytes + read_at[t]);
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            x[t & 1][j] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ((wm * MT + j) * 32) * kStepBytes + read_at[t]);
+            x[AHEAD ? t & 1 : 0][j] = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ((wm * MT + j) * 32) * kStepBytes + read_at[t]);
         }
     };
     // scale bytes of one step of the group; byte 0 and 2 of a word are the lane's
@@ -454,7 +479,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     load_codes(STAGES - 1);
     ++load_step;
     read_scales(0, 0, 0);
-    read_codes(0, 0);
+    if (AHEAD) read_codes(0, 0);
     int buffer = 0;
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
@@ -478,7 +503,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
                             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                operand(w[t & 1][i]), operand(x[t & 1][j]), acc[i][j], kE2M1, kE2M1, 2 * (t & 1),
+                                operand(w[AHEAD ? t & 1 : 0][i]), operand(x[AHEAD ? t & 1 : 0][j]), acc[i][j], kE2M1, kE2M1, 2 * (t & 1),
                                 (int)sw[s & 1][i][t >> 1], 2 * (t & 1), (int)sa[s & 1][j][t >> 1]);
                             // keeps the product in this place: without it the compiler moves the
                             // products of a step behind the branches and reads that follow
@@ -490,20 +515,21 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                 // reads stand before the products that they hide behind; unfenced they sink to their use
                 constexpr int LAST = kGroupSteps - 1;
                 const int next_buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
-                read_codes(s % STAGES, 1);
+                read_codes(s % STAGES, AHEAD ? 1 : 0);
                 if (s == LAST) store_scales(next_buffer);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 0>{});
-                read_codes(s % STAGES, 2);
+                read_codes(s % STAGES, AHEAD ? 2 : 1);
                 if (s < LAST) read_scales((s + 1) & 1, buffer, s + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 1>{});
-                read_codes(s % STAGES, 3);
+                read_codes(s % STAGES, AHEAD ? 3 : 2);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 2>{});
+                if (!AHEAD) read_codes(s % STAGES, 3);
                 // the next step has landed once no more than the loads behind it are left
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
-                read_codes((s + 1) % STAGES, 0);
+                if (AHEAD) read_codes((s + 1) % STAGES, 0);
                 if (s == LAST) read_scales(0, next_buffer, 0);
                 __builtin_amdgcn_sched_barrier(0);
                 // the step loaded here is STAGES ahead: the first of a group brings the group's scales
