@@ -582,19 +582,24 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tile by the mean rows of an expert that has some and by the rounds that the
-// tiles make on the CUs.  Measured in us, weights out of cache, K = 2048 unless
-// said otherwise:
-//   E 8, N 4096:  rows    8: 32x64 8.2, 64x128 9.6;    rows  128: 10.6, 12.3
-//                 rows  512: 32x64 16.2, 64x128 14.1, 128x128 16.0
-//                 rows 1024: 64x128 22.8, 128x128 19.0
-//   E 1, N 2048:  rows 1024: 64x128 8.7, 128x128 10.0 (too few tiles for the CUs)
-//   E 512, N 1536: rows  60: 32x64 with four stages 20.8, with two 25.0
-//   E 512, N 2048, K 768: rows 512: 32x64 with two stages 50.3, 64x128 49.1
-// The four-stage form loads up to a tile ahead, so K must make two groups.
+// Tile by the mean rows of an expert that has some, by how many tiles that makes
+// for 256 CUs, and in the end by the rounds that they take.  Measured in us,
+// weights out of cache, stages in brackets:
+//                                32x64 [4]  64x128 [4]  64x128 [2]  128x128 [2]
+//   E 1, N 4096, K 14336, rows 64   18.8       30.5        45.4        48.7
+//   E 1, N 4096, K 4096, rows 256   10.1       11.5        13.3        15.2
+//                        rows 512   15.5       12.2        13.9        15.5
+//   E 8, N 4096, K 4096, rows 256   21.6       17.8        20.5        21.9
+//                        rows 512   30.1       23.7        23.1        27.7
+//                        rows 1024  42.7       34.5        38.2        29.9
+//   E 8, N 4096, K 2048, rows 128   10.6        -          12.3        13.2
+//                        rows 1024   -          -          22.8        19.0
+//   E 512, N 1536, K 2048, rows 60  20.8        -          21.0        23.9
+//   E 512, N 2048, K 768, rows 512  50.3 [2]    -          49.1        52.9
+// The four-stage forms load up to a tile ahead, so K must make two groups.
 // A round of 256 x 256 (one a CU) takes 1.6 times as long as one of 128 x 128
 // (two a CU), for twice the work; rounds of either, and the time of both:
-//   E 8, N 4096:          rows 4096: 2 and 3, 42.1 and 35.7;  rows 8192: 3 and 5, 64.6 and 63.3
+//   E 8, N 4096, K 2048:  rows 4096: 2 and 3, 42.1 and 35.7;  rows 8192: 3 and 5, 64.6 and 63.3
 //   E 8, N 8192, K 4096:  rows 2048: 2 and 3, 83.8 and 66.7;  rows 4096: 3 and 5, 99.3 and 109.6
 //   E 1, N 4096, K 4096:  rows 4096: 1 and 2, 43.6 and 51.5;  rows 8192: 2 and 4, 84.7 and 110.9
 template <int DT>
@@ -606,7 +611,10 @@ hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
         const int64_t m = experts == 1 ? (a.rows + bm - 1) / bm : a.rows / bm + (experts + 1) / 2;
         return m * ((a.N + bn - 1) / bn);
     };
-    if (mean <= 16 && a.K > 1024) return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
+    if (a.K > 1024) {
+        if (mean <= 16 || tiles(32, 64) <= 2 * kCUs) return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
+        if (tiles(64, 128) <= kCUs) return launch_tiled<DT, 1, 2, 2, 2, 4>(a, 1, s);
+    }
     const int64_t middle = tiles(128, 128);
     if (mean <= 64 || middle < kCUs) return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
     const int64_t middle_rounds = (middle + 2 * kCUs - 1) / (2 * kCUs);

@@ -189,6 +189,10 @@ PRODUCT = [
     (1000, 2, 3, 2080, 264, BF16, True, 0.0),
     (1500, 1, 1, 512, 640, F16, False, 0.0),
     (9, 1, 2, 64, 5000, BF16, False, 0.5),
+    (300, 1, 1, 2080, 2000, BF16, False, 0.0),   # few tiles, long K: four stages, 64 x 128
+    (250, 2, 8, 2048, 1100, F32, True, 0.1),
+    (120, 1, 2, 3808, 700, F16, False, 0.0),
+    (33, 1, 1, 8192, 130, BF16, False, 0.0),
 ]
 
 
