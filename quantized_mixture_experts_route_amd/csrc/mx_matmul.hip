@@ -587,11 +587,13 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 // weights out of cache, stages in brackets:
 //                                32x64 [4]  64x128 [4]  64x128 [2]  128x128 [2]
 //   E 1, N 4096, K 14336, rows 64   18.8       30.5        45.4        48.7
+//                        rows 1024  92.3       59.6        53.5        53.7 (43.4 with four stages)
 //   E 1, N 4096, K 4096, rows 256   10.1       11.5        13.3        15.2
 //                        rows 512   15.5       12.2        13.9        15.5
 //   E 8, N 4096, K 4096, rows 256   21.6       17.8        20.5        21.9
 //                        rows 512   30.1       23.7        23.1        27.7
 //                        rows 1024  42.7       34.5        38.2        29.9
+//   E 8, N 2048, K 4096, rows 1024   -         23.6        22.9        20.9 (18.0)
 //   E 8, N 4096, K 2048, rows 128   10.6        -          12.3        13.2
 //                        rows 1024   -          -          22.8        19.0
 //   E 512, N 1536, K 2048, rows 60  20.8        -          21.0        23.9
@@ -611,11 +613,12 @@ hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
         const int64_t m = experts == 1 ? (a.rows + bm - 1) / bm : a.rows / bm + (experts + 1) / 2;
         return m * ((a.N + bn - 1) / bn);
     };
+    const int64_t middle = tiles(128, 128);
     if (a.K > 1024) {
         if (mean <= 16 || tiles(32, 64) <= 2 * kCUs) return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
         if (tiles(64, 128) <= kCUs) return launch_tiled<DT, 1, 2, 2, 2, 4>(a, 1, s);
+        if (mean > 64 && middle <= kCUs) return launch_tiled<DT, 2, 2, 2, 2, 4>(a, 1, s);
     }
-    const int64_t middle = tiles(128, 128);
     if (mean <= 64 || middle < kCUs) return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
     const int64_t middle_rounds = (middle + 2 * kCUs - 1) / (2 * kCUs);
     const int64_t large_rounds = (tiles(256, 256) + kCUs - 1) / kCUs;

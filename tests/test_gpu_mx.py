@@ -193,6 +193,8 @@ PRODUCT = [
     (250, 2, 8, 2048, 1100, F32, True, 0.1),
     (120, 1, 2, 3808, 700, F16, False, 0.0),
     (33, 1, 1, 8192, 130, BF16, False, 0.0),
+    (1100, 1, 4, 2112, 1600, BF16, True, 0.05),  # four stages, 128 x 128
+    (1024, 1, 1, 4096, 3000, F16, False, 0.0),
 ]
 
 
