@@ -57,7 +57,7 @@ __device__ inline i32x8 operand(u32x4 v)
 // scales go through registers, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 581 us, 3.3
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 568 us, 3.4
 // PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
 // instructions alone would take 354 us (power holds them at 1.8 GHz), loads
 // alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
@@ -73,6 +73,16 @@ constexpr uint32_t kOutside = 0x80000000u;  // a byte offset behind every buffer
 __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+
+// The lane, worked out where it stands.  Addresses made from it there need no register over the
+// K loop and the stores; those that the compiler keeps are spilled, and a reload waits for every
+// load and store before it.
+__device__ inline int lane_now()
+{
+    int zero = 0;
+    asm volatile("" : "+s"(zero));
+    return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
 }
 
 // 16 bytes a lane from the buffer to LDS at `to` + 16 * lane (to is uniform).
@@ -97,11 +107,11 @@ __device__ inline uint32_t pack_pair(float lo, float hi)
 // 8 q + 4 half + i in register 4 q + i.  `out` is the block's first row and
 // column; rows and cols say how many of them exist (WHOLE: all 32).
 template <int DT, bool WHOLE>
-__device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int rows, int cols, const f32x16& acc)
+__device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int rows, int cols, const f32x16& acc, int lane)
 {
     typedef typename RowType<DT>::Raw Raw;
     constexpr int V = 16 / sizeof(Raw);
-    const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
+    const int c = lane & 31, half = lane >> 5;
     auto store = [&](int row, int col, const u32x4& v) {
         if (!WHOLE && row >= rows) return;
         RowVec<Raw, V> y;
@@ -235,6 +245,13 @@ __device__ void build_tile_list(int* first, int* scratch, const int32_t* offsets
     __syncthreads();
 }
 
+// Reads through it are scalar and wait for no vector memory; what it points to does not change
+// while the kernel runs.
+__device__ inline const __attribute__((address_space(4))) int32_t* constant(const int32_t* p)
+{
+    return (const __attribute__((address_space(4))) int32_t*)p;
+}
+
 struct TileItem {
     int expert;
     int row0;
@@ -271,6 +288,11 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     constexpr int LOADS = ROWS / 8 / WAVES;     // code loads of a wavefront and step: 8 rows each
     constexpr int LOADS_A = BM / 8 / WAVES;
     constexpr int SCALE_LOADS = (ROWS / 32 + WAVES - 1) / WAVES;  // scale loads: 32 rows each
+    // The tile that fills the registers: addresses by lane_now, the next item found in a tile's last
+    // steps, and a tile's first barrier does not wait for the stores of the tile before it (8192 x
+    // 28672 x 4096 over 8 experts: 583 -> 567 us).  With scales through registers it gained nothing.
+    constexpr bool FULL = WHOLE && MT * NT >= 8;
+    static_assert(!FULL || (STAGES == 2 && BM <= THREADS), "one route a thread, taken behind start_tile");
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && WAVES % 2 == 0, "load split");
 
     // one array for all of it: between arrays of their own the compiler tells apart what a load to
@@ -283,7 +305,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     int* const first = reinterpret_cast<int*>(lds + LIST);
     int* const source = reinterpret_cast<int*>(lds + SOURCE);
 
-    const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
+    const int lane = threadIdx.x & 63;
+    auto lane_here = [&]() { return FULL ? lane_now() : lane; };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int K2 = a.K / 2, blocks = a.K / 32;
@@ -317,38 +340,37 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     // ---- the loading side: an item and a step, up to STAGES steps ahead
     TileItem load_tile;
     int load_step = 0;
-    const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+    auto load_chunk = [&](int id) { return (uint32_t)((id & 7) ^ ((wave & 1) * 4 + (id >> 4))) * 16; };
+    auto scale_chunk = [](int id) { return (uint32_t)((id & 1) ^ ((id >> 4) & 1)) * 16; };
     uint32_t code_at[LOADS_A];      // byte offset of the lane's chunk at step 0
-    const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk;  // rows behind N: out of bounds
+    const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk(lane);  // rows behind N: out of bounds
     uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's half of a scale row's group
-    const uint32_t scale_chunk = ((lane & 1) ^ ((lane >> 4) & 1)) * 16;
     __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
     const uint8_t *a_scale_base = nullptr, *w_scale_base = nullptr;
 
     // The next item, and in LDS its rows' source rows in a (from the tile's first row where there
-    // are no routes; -1: outside; rows behind the tile's repeat its last).  Found while no product is
-    // pending: registers are free then, and the reads wait for nothing but loads of the last steps.
+    // are no routes; -1: outside; rows behind the tile's repeat its last).  Found between two tiles,
+    // where registers are free; FULL: in the tile's last steps, so that the routes are there by then.
     TileItem next_tile;
     int found = 0;  // tables of source rows take turns
     auto find_tile = [&](auto offset) {
         next_tile = item_at<BM, BN>(first, offset, a.E, n_tiles, next_item, end);
         next_item += per_die;
+        found ^= BM;
+    };
+    auto offset_of = [&](int e) { return a.offsets ? min(max(constant(a.offsets)[e], 0), a.rows) : e * a.rows; };
+    auto route_of = [&](int r) {
+        r = min(r, next_tile.n - 1);
+        return a.sorted_routes ? a.sorted_routes[next_tile.row0 + r] : r;
+    };
+    auto set_source = [&](int r, int route) {
+        if (a.sorted_routes) route = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
+        source[found + r] = route;
     };
     auto find_rows = [&]() {
-        found ^= BM;
-        for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
-            int src = min(r, next_tile.n - 1);
-            if (a.sorted_routes) {
-                const int route = a.sorted_routes[next_tile.row0 + src];
-                src = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
-            }
-            source[found + r] = src;
-        }
+        for (int r = wave * kWave + lane_here(); r < BM && next_tile.n > 0; r += THREADS) set_source(r, route_of(r));
     };
-    auto find_item = [&]() {
-        find_tile([&](int e) { return a.offsets ? min(max(a.offsets[e], 0), a.rows) : e * a.rows; });
-        find_rows();
-    };
+    int route = 0;  // FULL: on its way from the tile's last steps on
     auto start_tile = [&]() {  // all but what goes by the source rows
         load_tile = next_tile;
         load_step = 0;
@@ -366,17 +388,18 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         as_buf = buffer_of(a_scale_base, (uint32_t)(a_rows * blocks));
     };
     auto start_rows = [&]() {
+        const int id = lane_here();
         const int w_rows = min(BN, a.N - load_tile.n0);
 #pragma unroll
         for (int j = 0; j < LOADS_A; ++j) {
-            const int row = source[found + (j * WAVES + wave) * 8 + (lane >> 3)];
-            code_at[j] = row < 0 ? kOutside : row * (uint32_t)K2 + load_chunk;
+            const int row = source[found + (j * WAVES + wave) * 8 + (id >> 3)];
+            code_at[j] = row < 0 ? kOutside : row * (uint32_t)K2 + load_chunk(id);
         }
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
-            const int row = r0 < BM ? source[found + r0 + (lane >> 1)] : min(r0 - BM + (lane >> 1), w_rows - 1);
-            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + scale_chunk;
+            const int row = r0 < BM ? source[found + r0 + (id >> 1)] : min(r0 - BM + (id >> 1), w_rows - 1);
+            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + scale_chunk(id);
         }
     };
     // codes of the loading side's step into stage `stage`; loads [from, to) of the wavefront
@@ -386,7 +409,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         for (int j = decltype(from)::value; j < decltype(to)::value; ++j) {
             uint32_t off = j < LOADS_A ? code_at[j < LOADS_A ? j : 0] : w_at + (uint32_t)((j - LOADS_A) * WAVES * 8) * K2;
             if constexpr (!WHOLE) {
-                if (at + load_chunk >= (uint32_t)K2) off = kOutside;
+                if (at + load_chunk(lane) >= (uint32_t)K2) off = kOutside;
             }
             load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
         }
@@ -407,7 +430,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             } else {
                 u32x4 v = {};
                 if (load_tile.n > 0 && scale_at[j] != kOutside) {
-                    const int chunk = at + scale_chunk;
+                    const int chunk = at + scale_chunk(lane);
                     v = load_scale_chunk((r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at, chunk, blocks - chunk);
                 }
                 scale_regs[j] = v;
@@ -440,15 +463,21 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         load_codes(i);
         ++load_step;
     }
-    find_item();
+    find_tile(offset_of);
+    find_rows();
 
-    // chunk 2 t + half of row c
-    uint32_t read_at[4];
+    // addresses of the reads: chunk 2 t + half of row c
+    uint32_t read_at[4], scales_at, half8;
+    auto set_reads = [&]() {
+        const int id = lane_here(), row = id & 31, high = id >> 5;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) read_at[t] = c * (uint32_t)kStepBytes + (((2 * t + half) ^ ((c >> 1) & 7)) * 16);
+        for (int t = 0; t < 4; ++t) read_at[t] = row * (uint32_t)kStepBytes + (((2 * t + high) ^ ((row >> 1) & 7)) * 16);
+        scales_at = row * kScaleBytes + ((row >> 3) & 1) * 16;
+        half8 = 8 * high;
+    };
+    set_reads();
     // Operands of two quarters.  The largest tile with scales through registers has no room for them:
-    // spilled registers wait for the loads in flight, so there a quarter's operands are read right
-    // before it (8192 x 16384 x 4064: 456 -> 412 us).
+    // there a quarter's operands are read right before it (8192 x 16384 x 4064: 456 -> 412 us).
     constexpr bool AHEAD = WHOLE || MT * NT < 8;
     u32x4 w[AHEAD ? 2 : 1][NT], x[AHEAD ? 2 : 1][MT];
     u32x2 sw[2][NT], sa[2][MT];
@@ -463,16 +492,15 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         }
     };
     // scale bytes of one step of the group; byte 0 and 2 of a word are the lane's
-    const uint32_t scales_at = c * kScaleBytes + ((c >> 3) & 1) * 16;
     auto read_scales = [&](int to, int buffer, int step) {
         const uint8_t* from = scales + buffer * ROWS * kScaleBytes + (scales_at ^ (step / 2 * 16)) + step % 2 * 8;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            sw[to][i] = *reinterpret_cast<const u32x2*>(from + (BM + (wn * NT + i) * 32) * kScaleBytes) >> (8 * half);
+            sw[to][i] = *reinterpret_cast<const u32x2*>(from + (BM + (wn * NT + i) * 32) * kScaleBytes) >> half8;
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-            sa[to][j] = *reinterpret_cast<const u32x2*>(from + ((wm * MT + j) * 32) * kScaleBytes) >> (8 * half);
+            sa[to][j] = *reinterpret_cast<const u32x2*>(from + ((wm * MT + j) * 32) * kScaleBytes) >> half8;
         }
     };
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
@@ -481,8 +509,15 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     read_scales(0, 0, 0);
     if (AHEAD) read_codes(0, 0);
     int buffer = 0;
+    // Stores count with the loads, in order of issue.  The loads that a tile's first barrier waits for
+    // were issued before the stores of the tile before it, which may run on there: `stored` says that
+    // there were at least STORES of them (no block was cut).
+    constexpr int STORES = MT * NT * (DT == kF32 ? 4 : 2);
+    static_assert((STAGES - 2) * LOADS + STORES < 64, "the counter's range");
+    bool stored = false;
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
+        set_reads();
         // wavefronts whose rows lie behind the tile's leave their products out; the two wavefronts of
         // a SIMD hold different row blocks, so a half-full tile takes half the time
         const bool active = wm * MT * 32 < tile.n;
@@ -528,10 +563,20 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                 multiply(std::integral_constant<int, 2>{});
                 if (!AHEAD) read_codes(s % STAGES, 3);
                 // the next step has landed once no more than the loads behind it are left
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
+                if (FULL && s == 0 && stored) {
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS + STORES) : "memory");
+                    stored = false;
+                } else {
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS) : "memory");
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 if (AHEAD) read_codes((s + 1) % STAGES, 0);
                 if (s == LAST) read_scales(0, next_buffer, 0);
                 __builtin_amdgcn_sched_barrier(0);
+                if (FULL && s == kGroupSteps - 2 && load_step < kGroupSteps) {
+                    find_tile(offset_of);
+                    if (next_tile.n > 0 && wave * kWave < BM) route = route_of(wave * kWave + lane_now());
+                }
                 // the step loaded here is STAGES ahead: the first of a group brings the group's scales
                 if (s == kGroupSteps - STAGES) load_scales(next_buffer);
                 load_codes(s % STAGES);
@@ -544,7 +589,14 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             }
             buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
         }
-        find_item();
+        const int id = lane_here();
+        if constexpr (FULL) {
+            if (next_tile.n > 0 && wave * kWave < BM) set_source(wave * kWave + id, route);
+        } else {
+            find_tile(offset_of);
+            find_rows();
+        }
+        stored = tile.n >= (wm * MT + MT) * 32 && a.N - tile.n0 >= (wn * NT + NT) * 32;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int m0 = (wm * MT + j) * 32;
@@ -553,9 +605,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                 const int n = tile.n0 + (wn * NT + i) * 32;
                 Raw* out = (Raw*)a.out + (int64_t)(tile.row0 + m0) * a.N + n;
                 if (tile.n - m0 >= 32 && a.N - n >= 32) {
-                    store_block<DT, true>(out, a.N, 32, 32, acc[i][j]);
+                    store_block<DT, true>(out, a.N, 32, 32, acc[i][j], id);
                 } else {
-                    store_block<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j]);
+                    store_block<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j], id);
                 }
             }
         }
