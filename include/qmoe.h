@@ -343,7 +343,8 @@ int qmoe_forward_ex(const void* hidden, const float* logits, int64_t T, int32_t 
  *                   for a dropped one
  *   workspace       >= qmoe_permute_workspace_size(T, top_k, E) bytes, 4-byte
  *                   aligned; contents on entry do not matter (the size is 0
- *                   for few routes, then workspace may be NULL)
+ *                   for few routes, then workspace may be NULL); calls that may
+ *                   run at once, replayed ones too, need one each
  * Requires 1 <= E <= 1024, 1 <= top_k <= 1024 (not bounded by E), T < 2^23,
  * T*top_k < 2^31, 1 <= H <= 2^20; dtype F16, BF16 or F32.  T = 0 writes the
  * offsets (all 0).  Rows are copied bit for bit.  The gradient with respect to
@@ -363,7 +364,8 @@ int qmoe_permute(const void* hidden, int64_t row_stride, int64_t T, int32_t H, i
  *   rows        dtype [T*top_k, H], rows row_stride elements apart
  *   route_rows  int32 [T, top_k] as qmoe_permute writes it
  *   weights     float32 [T, top_k], or NULL: every weight is 1
- *   out         dtype [T, H] out; a token without kept routes gets zeros
+ *   out         dtype [T, H] out, not overlapping rows; a token without kept
+ *               routes gets zeros
  * Sizes as qmoe_permute.  T = 0 returns QMOE_OK and enqueues nothing.
  */
 int qmoe_unpermute(const void* rows, int64_t row_stride, const int32_t* route_rows,
@@ -382,7 +384,8 @@ int qmoe_unpermute(const void* rows, int64_t row_stride, const int32_t* route_ro
  *                 grad_out[t] with the route's row, float32 sums in a fixed
  *                 order; 0 for a dropped route
  * Every row of grad_rows is written once when route_rows is qmoe_permute's (no
- * row twice); rows that no entry of another table names are left as they were.
+ * row twice).  With another table, rows that no entry names are left as they
+ * were, and a row that several name holds any one's gradient.
  * grad_rows must not overlap grad_out or rows.
  */
 int qmoe_unpermute_backward(const void* grad_out, int64_t grad_stride, const void* rows,

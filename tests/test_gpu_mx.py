@@ -442,3 +442,27 @@ def test_layer_of_the_operators_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(captured, want)
+
+
+def test_two_calls_at_once():
+    # two streams, the same weights, each with its own tokens: as one after the other
+    T, H, I, E, k = 700, 512, 256, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w1 = qm.mx_quantize(torch.randn(E, 2 * I, H, generator=g, device="cuda") * H ** -0.5)
+    w2 = qm.mx_quantize(torch.randn(E, H, I, generator=g, device="cuda") * I ** -0.5)
+    sets = []
+    for _ in range(2):
+        ids, wts = qm.route(torch.randn(T, E, generator=g, device="cuda"), k)
+        sets.append((torch.randn(T, H, generator=g, device="cuda").to(BF16), ids, wts))
+    want = [_mx_layer(*t, w1, w2, E, k) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(_mx_layer(*sets[i], w1, w2, E, k))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for each in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(each, want[i]))
