@@ -57,14 +57,14 @@ __device__ inline i32x8 operand(u32x4 v)
 // scales go through registers, and codes
 // behind the row's end are read out of the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 568 us, 3.4
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 558 us, 3.4
 // PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
 // instructions alone would take 354 us (power holds them at 1.8 GHz), loads
 // alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
 // storing 470 MB adds 100 us: the three overlap in part only, since one
-// workgroup fills a CU.  8192^3, one expert: 275 us, 4.0 PFLOP/s.  Rows that
-// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 412 us, K =
-// 4096 339.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
+// workgroup fills a CU.  8192^3, one expert: 246 us, 4.5 PFLOP/s.  Rows that
+// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 370 us, K =
+// 4096 303.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row
@@ -252,6 +252,11 @@ __device__ inline const __attribute__((address_space(4))) int32_t* constant(cons
     return (const __attribute__((address_space(4))) int32_t*)p;
 }
 
+// The workgroups that run on a die at a time (32 of the largest tile) share rows and weights in its
+// L2: bands of 8 m-tiles make that about 8 row blocks and 4 weight blocks, in place of one column of
+// 32 (8192^3: 281 -> 246 us; bands of 4 and of 12 were slower).
+constexpr int kBand = 8;
+
 struct TileItem {
     int expert;
     int row0;
@@ -272,10 +277,19 @@ __device__ TileItem item_at(const int* first, Offset offset, int E, int n_tiles,
     lo = __builtin_amdgcn_readfirstlane(lo);
     const int base = __builtin_amdgcn_readfirstlane(first[lo]);
     const int m_tiles = __builtin_amdgcn_readfirstlane(first[lo + 1]) - base;
-    const int local = item - base * n_tiles;
-    const int nt = local / m_tiles;  // neighbouring items share the weights
+    // bands of up to kBand m-tiles, in a band neighbouring items share the weights
+    int local = item - base * n_tiles;
+    int m0 = 0, band = m_tiles;
+    if (m_tiles > kBand) {
+        const int bands = (m_tiles + kBand - 1) / kBand;
+        band = (m_tiles + bands - 1) / bands;
+        m0 = local / (band * n_tiles) * band;
+        local -= m0 * n_tiles;
+        band = min(band, m_tiles - m0);
+    }
+    const int nt = local / band;
     const int r_lo = offset(lo), r_hi = offset(lo + 1);
-    const int row0 = r_lo + (local - nt * m_tiles) * BM;
+    const int row0 = r_lo + (m0 + local - nt * band) * BM;
     return TileItem{lo, row0, min(BM, r_hi - row0), nt * BN};
 }
 
@@ -477,7 +491,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     };
     set_reads();
     // Operands of two quarters.  The largest tile with scales through registers has no room for them:
-    // there a quarter's operands are read right before it (8192 x 16384 x 4064: 456 -> 412 us).
+    // there a quarter's operands are read right before it (8192 x 16384 x 4064: 456 -> 412 us
+    // when it was taken up).
     constexpr bool AHEAD = WHOLE || MT * NT < 8;
     u32x4 w[AHEAD ? 2 : 1][NT], x[AHEAD ? 2 : 1][MT];
     u32x2 sw[2][NT], sa[2][MT];
@@ -653,9 +668,10 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
 // The four-stage forms load up to a tile ahead, so K must make two groups.
 // A round of 256 x 256 (one a CU) takes 1.6 times as long as one of 128 x 128
 // (two a CU), for twice the work; rounds of either, and the time of both:
-//   E 8, N 4096, K 2048:  rows 4096: 2 and 3, 42.1 and 35.7;  rows 8192: 3 and 5, 64.6 and 63.3
-//   E 8, N 8192, K 4096:  rows 2048: 2 and 3, 83.8 and 66.7;  rows 4096: 3 and 5, 99.3 and 109.6
-//   E 1, N 4096, K 4096:  rows 4096: 1 and 2, 43.6 and 51.5;  rows 8192: 2 and 4, 84.7 and 110.9
+//   E 8, N 4096, K 2048:  rows 4096: 2 and 3, 43.0 and 37.2;  rows 8192: 3 and 5, 65.4 and 64.3
+//   E 8, N 8192, K 4096:  rows 2048: 2 and 3, 71.1 and 67.5;  rows 4096: 3 and 5, 99.8 and 115.7
+//   E 1, N 4096, K 4096:  rows 4096: 1 and 2, 40.5 and 43.9;  rows 8192: 2 and 4, 71.5 and 81.2
+//   E 1, N 8192, K 8192:  rows 4096: 2 and 4, 133.5 and 182.1
 template <int DT>
 hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
 {
