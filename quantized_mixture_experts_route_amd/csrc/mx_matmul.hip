@@ -54,14 +54,15 @@ __device__ inline i32x8 operand(u32x4 v)
 //
 // WHOLE: K is a multiple of 1024 and the scale rows are 16-byte aligned, so
 // scales take the direct path to LDS too and no step has a tail.  Otherwise
-// scales go through registers, and codes
-// behind the row's end are read out of the buffer's bounds, which gives 0.
+// scales go through registers, and codes behind the row's end are read out of
+// the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 558 us, 3.4
-// PFLOP/s.  The matrix units are busy 40% of the cycles at 2.0 GHz; matrix
-// instructions alone would take 354 us (power holds them at 1.8 GHz), loads
-// alone 325 us (64 KB a step and CU; 180 us where all of it is in L2), and
-// storing 470 MB adds 100 us: the three overlap in part only, since one
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 559 us, 3.4
+// PFLOP/s, 1.1 million cycles with the matrix units busy 43% of them, at about
+// 2.0 GHz: power holds the clock down, and a step that took out a sixth of the
+// cycles gained 4% of the time.  Matrix instructions alone would take 354 us (at
+// 1.8 GHz), loads alone 325 us (64 KB a step and CU; 180 us where all of it is
+// in L2), and storing 470 MB adds 100 us: the three overlap in part, since one
 // workgroup fills a CU.  8192^3, one expert: 246 us, 4.5 PFLOP/s.  Rows that
 // do not start on lines cost more: K = 4064 at N 16384, 8192 rows 370 us, K =
 // 4096 303.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
@@ -491,8 +492,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     };
     set_reads();
     // Operands of two quarters.  The largest tile with scales through registers has no room for them:
-    // there a quarter's operands are read right before it (8192 x 16384 x 4064: 456 -> 412 us
-    // when it was taken up).
+    // there a quarter's operands are read right before it (8192 x 16384 x 4064: 456 -> 412 us when taken up).
     constexpr bool AHEAD = WHOLE || MT * NT < 8;
     u32x4 w[AHEAD ? 2 : 1][NT], x[AHEAD ? 2 : 1][MT];
     u32x2 sw[2][NT], sa[2][MT];
