@@ -46,16 +46,17 @@ __device__ inline i32x8 operand(u32x4 v)
 // is one buffer: its last read is behind the group's second barrier, the next
 // group's load is issued behind the third and has landed at the fourth.  With
 // four stages there are two, loaded a group ahead.  A lane reads 8 bytes a step
-// and picks its byte by shift and operand select.
+// and picks its byte by shift and operand select.  With two stages a tile may end
+// behind half a group (8192 x 8192 x 1536 over 8 experts: 108 -> 99 us).
 //
 // LDS rows are 128 bytes (32 banks); the 16-byte chunk of row r sits in slot
 // chunk ^ (r / 2 % 8), so that 16 rows read at one chunk cover all 64 banks.
 // Scale rows of 32 bytes swap their halves where r / 8 is odd.
 //
-// WHOLE: K is a multiple of 1024 and the scale rows are 16-byte aligned, so
-// scales take the direct path to LDS too and no step has a tail.  Otherwise
-// scales go through registers, and codes behind the row's end are read out of
-// the buffer's bounds, which gives 0.
+// WHOLE: K fills its steps (a multiple of 1024, with two stages of 512 from 1024
+// on) and the scale rows are 16-byte aligned, so scales take the direct path to
+// LDS too and no step has a tail.  Otherwise scales go through registers, and
+// codes behind the row's end are read out of the buffer's bounds, which gives 0.
 //
 // What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 559 us, 3.4
 // PFLOP/s, 1.1 million cycles with the matrix units busy 43% of them, at about
@@ -325,7 +326,11 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int K2 = a.K / 2, blocks = a.K / 32;
-    const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps;  // whole groups
+    // whole groups of steps; with two stages the last may be half a group, but not the only one: the
+    // loading side is two steps ahead and would be at its end before the tile begins
+    const int filled = (a.K + 255) / 256;
+    const bool half_group = STAGES == 2 && filled > 2 && (filled - 1) % kGroupSteps < 2;
+    const int steps = (filled + kGroupSteps - 1) / kGroupSteps * kGroupSteps - (half_group ? 2 : 0);
 
     // the last stage's space, not loaded before the first barrier, holds the offsets for the first item
     int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
@@ -543,8 +548,10 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x16{};
         }
         for (int g = 0; g < steps; g += kGroupSteps) {
+            const bool half_g = half_group && g + 2 == steps;
 #pragma unroll
             for (int s = 0; s < kGroupSteps; ++s) {
+                const bool last = s == kGroupSteps - 1 || (s == 1 && half_g);  // of the group
                 auto multiply = [&](auto quarter) {
                     constexpr int t = decltype(quarter)::value;
                     if (!active || (!WHOLE && (g + s) * 256 + t * 64 >= a.K)) return;
@@ -563,14 +570,13 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                     __builtin_amdgcn_sched_barrier(0);
                 };
                 // reads stand before the products that they hide behind; unfenced they sink to their use
-                constexpr int LAST = kGroupSteps - 1;
                 const int next_buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
                 read_codes(s % STAGES, AHEAD ? 1 : 0);
-                if (s == LAST) store_scales(next_buffer);
+                if (last) store_scales(next_buffer);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 0>{});
                 read_codes(s % STAGES, AHEAD ? 2 : 1);
-                if (s < LAST) read_scales((s + 1) & 1, buffer, s + 1);
+                if (!last) read_scales((s + 1) & 1, buffer, s + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 multiply(std::integral_constant<int, 1>{});
                 read_codes(s % STAGES, AHEAD ? 3 : 2);
@@ -586,21 +592,23 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 if (AHEAD) read_codes((s + 1) % STAGES, 0);
-                if (s == LAST) read_scales(0, next_buffer, 0);
+                if (last) read_scales(0, next_buffer, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                if (FULL && s == kGroupSteps - 2 && load_step < kGroupSteps) {
+                if (FULL && s % 2 == 0 && load_step == 0) {
                     find_tile(offset_of);
                     if (next_tile.n > 0 && wave * kWave < BM) route = route_of(wave * kWave + lane_now());
                 }
                 // the step loaded here is STAGES ahead: the first of a group brings the group's scales
-                if (s == kGroupSteps - STAGES) load_scales(next_buffer);
+                if (s == kGroupSteps - STAGES || (s == 0 && half_g)) load_scales(next_buffer);
                 load_codes(s % STAGES);
                 multiply(std::integral_constant<int, 3>{});
                 ++load_step;
-                if ((s + STAGES) % kGroupSteps == LAST && load_step == steps) {  // tiles end with a group
+                // tiles end with a group or, of two stages, behind its half
+                if (((s + STAGES) % kGroupSteps == kGroupSteps - 1 || (STAGES == 2 && s == 3)) && load_step == steps) {
                     start_tile();
                     start_rows();
                 }
+                if (s == 1 && half_g) break;
             }
             buffer = SCALE_BUFFERS == 2 ? buffer ^ 1 : 0;
         }
@@ -642,7 +650,7 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
     const int64_t items = (experts + (a.rows - experts) / BM) * ((a.N + BN - 1) / BN);
     int64_t grid = (items + 7) / 8 * 8;
     if (grid > kCUs * wgs_per_cu) grid = kCUs * wgs_per_cu;
-    const bool whole = a.K % 1024 == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
+    const bool whole = a.K % (STAGES == 2 && a.K > 512 ? 512 : 1024) == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
     if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
     else launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);

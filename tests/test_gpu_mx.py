@@ -228,6 +228,14 @@ LARGE = [
     (2, 1312, 9001, [4097, 255], False, F32),
     (2, 96, 16390, [2000, 2400], True, F16),
     (4, 5120, 12288, [700, 900, 20, 1800], True, BF16),
+    # K that ends behind half a group of steps, in each of the tiles with two stages
+    (2, 1536, 16400, [2000, 2400], True, BF16),
+    (1, 2560, 16384, [4096], False, BF16),
+    (1, 3584, 12288, [4300], False, F32),
+    (4, 2304, 8200, [1500, 0, 2300, 700], True, F16),
+    (8, 1536, 4096, [128, 1, 255, 130, 0, 256, 129, 125], True, BF16),
+    (16, 1536, 8192, [50, 64, 1, 65, 63, 40, 0, 90] * 2, True, F16),
+    (16, 1312, 8190, [50, 64, 1, 65, 63, 40, 0, 90] * 2, False, F32),
 ]
 
 
