@@ -9,6 +9,7 @@
 // scale byte; the lane half h is the block of the two that the step contracts.
 // The result: register i of lane l is row 8 (i/4) + 4 h + i%4, column c.
 #include "expert_ops.h"
+#include "mx_shape.h"
 #include "qmoe_internal.h"
 #include "rowio.h"
 
@@ -70,12 +71,16 @@ __device__ inline i32x8 operand(u32x4 v)
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row
-constexpr uint32_t kOutside = 0x80000000u;  // a byte offset behind every buffer
 
-__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
-{
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
-}
+// Bytes of codes or scales that a tile reads; its descriptor from byte `at` on.
+struct Span {
+    const uint8_t* base;
+    uint32_t bytes;
+    __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
+    {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0, mx_bytes_left(bytes, at), 0x00020000);
+    }
+};
 
 // The lane, worked out where it stands.  Addresses made from it there need no register over the
 // K loop and the stores; those that the compiler keeps are spilled, and a reload waits for every
@@ -87,11 +92,11 @@ __device__ inline int lane_now()
     return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
 }
 
-// 16 bytes a lane from the buffer to LDS at `to` + 16 * lane (to is uniform).
-__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset, void* to)
+// 16 bytes a lane from the buffer to LDS at `to` + 16 * lane (to is uniform); zeros where the lane's
+// offset is not in the buffer.
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, void* to)
 {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, lane_offset,
-                                             offset, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, lane_offset, 0, 0, 0);
 }
 
 template <int DT>
@@ -365,8 +370,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     uint32_t code_at[LOADS_A];      // byte offset of the lane's chunk at step 0
     const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K2 + load_chunk(lane);  // rows behind N: out of bounds
     uint32_t scale_at[SCALE_LOADS]; // byte offset of the lane's half of a scale row's group
-    __amdgpu_buffer_rsrc_t a_buf, w_buf, as_buf, ws_buf;
-    const uint8_t *a_scale_base = nullptr, *w_scale_base = nullptr;
+    Span a_span, w_span, as_span, ws_span;  // codes and scales of the loading side's tile
 
     // The next item, and in LDS its rows' source rows in a (from the tile's first row where there
     // are no routes; -1: outside; rows behind the tile's repeat its last).  Found between two tiles,
@@ -398,14 +402,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
         const bool on = t.n > 0;
         const int w_rows = on ? min(BN, a.N - t.n0) : 0;
         const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
-        w_buf = buffer_of(a.w_codes + w0 * K2, (uint32_t)(w_rows * K2));
-        w_scale_base = a.w_scales + w0 * blocks;
-        ws_buf = buffer_of(w_scale_base, (uint32_t)(w_rows * blocks));
+        w_span = Span{a.w_codes + w0 * K2, (uint32_t)(w_rows * K2)};
+        ws_span = Span{a.w_scales + w0 * blocks, (uint32_t)(w_rows * blocks)};
         const int64_t a0 = a.sorted_routes ? 0 : t.row0;
         const int64_t a_rows = !on ? 0 : a.sorted_routes ? a.a_rows : t.n;
-        a_buf = buffer_of(a.a_codes + a0 * K2, (uint32_t)(a_rows * K2));
-        a_scale_base = a.a_scales + a0 * blocks;
-        as_buf = buffer_of(a_scale_base, (uint32_t)(a_rows * blocks));
+        a_span = Span{a.a_codes + a0 * K2, (uint32_t)(a_rows * K2)};
+        as_span = Span{a.a_scales + a0 * blocks, (uint32_t)(a_rows * blocks)};
     };
     auto start_rows = [&]() {
         const int id = lane_here();
@@ -413,25 +415,26 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
 #pragma unroll
         for (int j = 0; j < LOADS_A; ++j) {
             const int row = source[found + (j * WAVES + wave) * 8 + (id >> 3)];
-            code_at[j] = row < 0 ? kOutside : row * (uint32_t)K2 + load_chunk(id);
+            code_at[j] = row < 0 ? kMxOutside : row * (uint32_t)K2 + load_chunk(id);
         }
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
             const int row = r0 < BM ? source[found + r0 + (id >> 1)] : min(r0 - BM + (id >> 1), w_rows - 1);
-            scale_at[j] = row < 0 ? kOutside : row * (uint32_t)blocks + scale_chunk(id);
+            scale_at[j] = row < 0 ? kMxOutside : row * (uint32_t)blocks + scale_chunk(id);
         }
     };
     // codes of the loading side's step into stage `stage`; loads [from, to) of the wavefront
     auto load_part = [&](int stage, auto from, auto to) {
         const uint32_t at = (uint32_t)load_step * kStepBytes;
+        const __amdgpu_buffer_rsrc_t a_buf = a_span.from(at), w_buf = w_span.from(at);
 #pragma unroll
         for (int j = decltype(from)::value; j < decltype(to)::value; ++j) {
             uint32_t off = j < LOADS_A ? code_at[j < LOADS_A ? j : 0] : w_at + (uint32_t)((j - LOADS_A) * WAVES * 8) * K2;
             if constexpr (!WHOLE) {
-                if (at + load_chunk(lane) >= (uint32_t)K2) off = kOutside;
+                if (at + load_chunk(lane) >= (uint32_t)K2) off = kMxOutside;
             }
-            load_to_lds(j < LOADS_A ? a_buf : w_buf, off, at, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
+            load_to_lds(j < LOADS_A ? a_buf : w_buf, off, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
         }
     };
     constexpr std::integral_constant<int, 0> kFirst;
@@ -441,17 +444,18 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     u32x4 scale_regs[WHOLE ? 1 : SCALE_LOADS];
     auto load_scales = [&](int buffer) {  // of the group that starts at the loading side's step
         const int at = load_step * 8;
+        const __amdgpu_buffer_rsrc_t as_buf = as_span.from(at), ws_buf = ws_span.from(at);
 #pragma unroll
         for (int j = 0; j < SCALE_LOADS; ++j) {
             const int r0 = (j * WAVES + wave) * 32;
             if (r0 >= ROWS) continue;
             if constexpr (WHOLE) {
-                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], at, scales + (buffer * ROWS + r0) * kScaleBytes);
+                load_to_lds(r0 < BM ? as_buf : ws_buf, scale_at[j], scales + (buffer * ROWS + r0) * kScaleBytes);
             } else {
                 u32x4 v = {};
-                if (load_tile.n > 0 && scale_at[j] != kOutside) {
+                if (load_tile.n > 0 && scale_at[j] != kMxOutside) {
                     const int chunk = at + scale_chunk(lane);
-                    v = load_scale_chunk((r0 < BM ? a_scale_base : w_scale_base) + scale_at[j] + at, chunk, blocks - chunk);
+                    v = load_scale_chunk((r0 < BM ? as_span.base : ws_span.base) + scale_at[j] + at, chunk, blocks - chunk);
                 }
                 scale_regs[j] = v;
             }

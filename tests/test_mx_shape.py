@@ -1,0 +1,40 @@
+"""The arithmetic behind the grouped MXFP4 product's loads and tiles (csrc/mx_shape.h), on the host."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from tests.test_host_sanitizers import CLANG, FLAGS, ROOT
+
+CSRC = os.path.join(ROOT, "quantized_mixture_experts_route_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def checker(tmp_path_factory):
+    if not os.path.exists(CLANG):
+        pytest.skip("ROCm clang++ not installed")
+    tmp = tmp_path_factory.mktemp("mx_shape")
+    obj, exe = str(tmp / "check.o"), str(tmp / "check")
+    for cmd in ([CLANG, *FLAGS, "-c", os.path.join(ROOT, "tests", "sanitize", "mx_shape_check.cpp"), "-o", obj],
+                [CLANG, "-fsanitize=address,undefined", obj, "-o", exe]):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        assert res.returncode == 0, res.stderr[-4000:]
+    return exe
+
+
+def test_shape_arithmetic(checker):
+    res = subprocess.run([checker], capture_output=True, text=True, timeout=120)
+    assert res.returncode == 0 and "checks passed" in res.stdout, res.stdout + res.stderr
+
+
+def test_loads_to_lds_carry_their_whole_offset_in_the_lane():
+    # the descriptor starts at the step and the scalar offset is 0: with the step in the scalar offset, the
+    # last scale row of an odd half group, and a step behind the last tile, were kept inside only by how the
+    # hardware adds that offset to its range comparison
+    text = open(os.path.join(CSRC, "mx_matmul.hip")).read()
+    calls = re.findall(r"raw_ptr_buffer_load_lds\(([^;]*)\);", text)
+    assert len(calls) == 1
+    offset, immediate, aux = (v.strip() for v in calls[0].split(",")[-3:])
+    assert (offset, immediate, aux) == ("0", "0", "0")
+    assert "mx_bytes_left(bytes, at)" in text
