@@ -430,7 +430,9 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *   a_codes, a_scales  [a_rows, K/2], [a_rows, K/32]
  *   w_codes, w_scales  [E, N, K/2], [E, N, K/32]
  *   expert_offsets     int32 [E+1], non-decreasing from 0: expert e(r) of the
- *                      rows [offsets[e], offsets[e+1]) (clamped to [0, rows]);
+ *                      rows [offsets[e], offsets[e+1]) (clamped to [0, rows];
+ *                      a table that decreases leaves values in out undefined,
+ *                      and nothing outside out is touched);
  *                      NULL only with E = 1: every row.  Rows from offsets[E]
  *                      on are set to zero.
  *   sorted_routes      NULL: src(r) = r (a_rows >= rows); or int32 [rows]:
@@ -441,8 +443,9 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *   out                dtype [rows, N] out (F16, BF16 or F32)
  * Scales of 255 (NaN) make the outputs they enter NaN.  expert_offsets must not
  * change while the call runs.  Requires 1 <= E <=
- * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24, and with
- * sorted_routes a_rows * K/2 < 2^31 (else QMOE_ERR_UNSUPPORTED).  rows = 0
+ * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24, rows * N at
+ * most 2^40, and with sorted_routes a_rows * K/2 < 2^31 (else
+ * QMOE_ERR_UNSUPPORTED).  rows = 0
  * returns QMOE_OK and enqueues nothing.
  */
 int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,

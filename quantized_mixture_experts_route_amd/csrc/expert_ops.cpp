@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "expert_ops.h"
+#include "mx_shape.h"
 #include "qmoe.h"
 #include "qmoe_internal.h"
 
@@ -286,6 +287,9 @@ int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_ro
     }
     if (rows >= (int64_t(1) << 24)) {
         return set_error(QMOE_ERR_UNSUPPORTED, "rows=%lld must be below 2^24", (long long)rows);
+    }
+    if (rows * N > qmoe::kMxMaxOutputs) {
+        return set_error(QMOE_ERR_UNSUPPORTED, "rows*N=%lld must be at most 2^40", (long long)(rows * N));
     }
     if (sorted_routes && a_rows > INT32_MAX / (K / 2)) {
         return set_error(QMOE_ERR_UNSUPPORTED, "a_codes read through sorted_routes must be below 2^31 bytes");

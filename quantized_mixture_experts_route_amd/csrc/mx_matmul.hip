@@ -221,8 +221,8 @@ __device__ inline u32x4 load_scale_chunk(const uint8_t* p, int chunk, int left)
 }
 
 // m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
-// Offsets are clamped to [0, rows], so no table content leads outside the
-// output.  scratch: E + 1 words of LDS.
+// Offsets are clamped to [0, rows] and mx_items() bounds the count, so no table
+// content leads outside the output.  scratch: E + 1 words of LDS.
 template <int BM, int THREADS>
 __device__ void build_tile_list(int* first, int* scratch, const int32_t* offsets, int E, int rows)
 {
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
     build_tile_list<BM, THREADS>(first, scratch, a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
-    const int total = first[a.E] * n_tiles;
+    const int total = mx_items(first[a.E], n_tiles, a.rows, BM, a.E);
     // workgroups go to the 8 dies in turn: each die takes one run of items, so
     // that the workgroups of a die share rows and weights in its L2
     const int per_die = gridDim.x / 8;

@@ -21,4 +21,15 @@ __host__ __device__ inline uint32_t mx_bytes_left(uint32_t bytes, uint32_t at)
     return left > 0 ? (uint32_t)left : 0u;
 }
 
+// Largest rows * N of a call: items (tiles of 32 x 64 or more) then count in 32 bits.
+constexpr int64_t kMxMaxOutputs = int64_t(1) << 40;
+
+// Items of `tiles` m-tiles of `bm` rows with n_tiles column tiles each.  Experts whose offsets do not
+// decrease have at most one partial tile each; a table with more tiles than that decreases somewhere, and
+// could count past 32 bits and lead the search for an item outside the output: it gets no items.
+__host__ __device__ inline int mx_items(int tiles, int n_tiles, int rows, int bm, int E)
+{
+    return tiles <= rows / bm + (E < rows ? E : rows) ? tiles * n_tiles : 0;
+}
+
 }  // namespace qmoe

@@ -56,10 +56,43 @@ void check_scale_rows()
     }
 }
 
+// Tables that do not decrease keep all their items; any table's items, and the products of a tile index
+// with the column tiles that the search forms, count in 32 bits.
+void check_items()
+{
+    const int tile[][2] = {{32, 64}, {64, 128}, {128, 128}, {256, 256}};
+    uint32_t seed = 1;
+    auto next = [&](uint32_t n) { return (seed = seed * 1664525u + 1013904223u) / 65536u % n; };
+    for (auto& t : tile) {
+        const int bm = t[0], bn = t[1];
+        for (int rows : {1, 31, 32, 33, 4096, 65536, (1 << 24) - 1}) {
+            for (int E : {1, 2, 7, 64, 1024}) {
+                int64_t N = qmoe::kMxMaxOutputs / rows;
+                if (N > 1 << 20) N = 1 << 20;
+                const int n_tiles = (int)((N + bn - 1) / bn);
+                int at = 0, tiles = 0;  // a random table that does not decrease
+                for (int e = 0; e < E; ++e) {
+                    const int to = e == E - 1 ? rows : at + (int)next((uint32_t)(rows - at) / 2 + 2);
+                    const int end = to < rows ? to : rows;
+                    tiles += (end - at + bm - 1) / bm;
+                    at = end;
+                }
+                EXPECT(qmoe::mx_items(tiles, n_tiles, rows, bm, E) == tiles * n_tiles);
+                EXPECT((int64_t)tiles * n_tiles <= INT32_MAX);
+                // every second expert with all the rows, the table falling back in between
+                const int64_t worst = (int64_t)(E + 1) / 2 * ((rows + bm - 1) / bm);
+                const int got = qmoe::mx_items((int)worst, n_tiles, rows, bm, E);
+                EXPECT(got >= 0 && (got == 0 || got == worst * n_tiles));
+            }
+        }
+    }
+}
+
 }  // namespace
 
 int main()
 {
+    check_items();
     check_bytes_left();
     check_scale_rows();
     std::printf("%ld checks passed\n", g_checks);

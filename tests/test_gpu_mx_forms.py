@@ -44,3 +44,15 @@ def test_neighbours_of_the_operands_do_not_matter(E, K, N, counts, gather):
     clean = qm.mx_matmul(*(t.clone() for t in (*a, *w)), _offsets(counts), sorted_routes=routes, top_k=1, dtype=BF16)
     assert not bool(torch.isnan(out).any())
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("rows,N,K", [(64, 40, 96), (600, 300, 1536)])
+def test_decreasing_offsets_stay_inside_the_output(rows, N, K):
+    # every second expert spans all rows: more tiles than any table that does not decrease can make
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    E = 64
+    a, w = _operand(g, rows, K), _operand(g, E, N, K)
+    off = torch.tensor([0, rows] * (E // 2) + [rows], dtype=torch.int32, device="cuda")
+    buf = torch.full((rows + 2, N), 7.0, device="cuda")
+    qm.mx_matmul(*a, *w, off, dtype=F32, out=buf[1:rows + 1])
+    assert buf[0].eq(7).all() and buf[-1].eq(7).all()

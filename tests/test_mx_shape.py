@@ -5,6 +5,7 @@ import subprocess
 
 import pytest
 
+import quantized_mixture_experts_route_amd as qm
 from tests.test_host_sanitizers import CLANG, FLAGS, ROOT
 
 CSRC = os.path.join(ROOT, "quantized_mixture_experts_route_amd", "csrc")
@@ -38,3 +39,16 @@ def test_loads_to_lds_carry_their_whole_offset_in_the_lane():
     offset, immediate, aux = (v.strip() for v in calls[0].split(",")[-3:])
     assert (offset, immediate, aux) == ("0", "0", "0")
     assert "mx_bytes_left(bytes, at)" in text
+
+
+def test_items_are_bounded_before_the_search():
+    # a decreasing table of 1024 experts over 65536 rows of 2^20 columns makes 2^32 items: the count wrapped
+    text = open(os.path.join(CSRC, "mx_matmul.hip")).read()
+    assert re.search(r"const int total = mx_items\(first\[a\.E\], n_tiles, a\.rows, BM, a\.E\);", text)
+
+
+def test_more_outputs_than_items_count_are_refused():
+    fake = 1 << 20
+    rc = qm.load_library().qmoe_mx_matmul(fake, fake, 1 << 23, fake, fake, 1, 1 << 20, 32, None, None, 1, 1 << 23, 2,
+                                          fake, None)
+    assert rc == qm.ERR_UNSUPPORTED and "2^40" in qm.last_error()
