@@ -476,6 +476,16 @@ def _rows(t, name: str, index: int, n: int) -> int:
     return stride if n > 1 else h
 
 
+_I32_MAX = (1 << 31) - 1
+
+
+def _fit(*sizes: int):
+    """Checks sizes that the library takes as 32-bit integers: ctypes would pass their low bits."""
+    for n in sizes:
+        if not -_I32_MAX <= n <= _I32_MAX:
+            raise QMoEError(ERR_UNSUPPORTED, f"qmoe: size {n} does not fit 32 bits")
+
+
 def _elsewhere(index: int, stream) -> bool:
     """Whether a call must be made under _on(): on a given stream or not on the current device."""
     return stream is not None or index != _current_device()
@@ -505,6 +515,7 @@ def _current(index: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def permute_workspace_size(T: int, top_k: int, E: int) -> int:
+    _fit(top_k, E)
     return int(load_library().qmoe_permute_workspace_size(T, top_k, E))
 
 
@@ -526,9 +537,11 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
     stride, H, dt, rows = 0, 0, DTYPE_F16, None
     if hidden is not None:
         stride, H, dt = _rows(hidden, "hidden", dev, T), hidden.shape[1], _row_dtype(hidden.dtype, "hidden")
+        if H > _I32_MAX:
+            _fit(H)
         rows = hidden.new_empty((R, H))
     lib = load_library()
-    need = permute_workspace_size(T, top_k, E)
+    need = permute_workspace_size(T, top_k, E)  # refuses a top_k or E of more than 32 bits
     if workspace is not None:
         _tensor(workspace, "workspace", dev, torch.uint8, workspace.shape)
     elif need:
@@ -555,6 +568,8 @@ def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[to
     at = _tensor(route_rows, "route_rows", dev, torch.int32, shape)
     stride, dt = _rows(rows, "rows", dev, T * top_k), _row_dtype(rows.dtype, "rows")
     H = rows.shape[1]
+    if H > _I32_MAX or top_k > _I32_MAX:
+        _fit(H, top_k)
     w = None if weights is None else _tensor(weights, "weights", dev, torch.float32, shape)
     if out is None:
         out = rows.new_empty((T, H))
@@ -584,6 +599,8 @@ def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], rou
     at = _tensor(route_rows, "route_rows", dev, torch.int32, shape)
     gstride, dt = _rows(grad_out, "grad_out", dev, T), _row_dtype(grad_out.dtype, "grad_out")
     H = grad_out.shape[1]
+    if H > _I32_MAX or top_k > _I32_MAX:
+        _fit(H, top_k)
     stride, grad_weights = 0, None
     if rows is not None:
         stride = _rows(rows, "rows", dev, T * top_k)
@@ -616,6 +633,7 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
             raise ValueError("x must have 2 or 3 dimensions to be quantised along its rows")
         _dev(x, "x")
         *lead, rows, K = x.shape
+        _fit(*lead, rows, K)
         codes = x.new_empty((*lead, K, rows // 2), dtype=torch.uint8)
         scales = x.new_empty((*lead, K, rows // MX_BLOCK), dtype=torch.uint8)
         _check(lib.qmoe_mx_quantize_columns(x.data_ptr(), lead[0] if lead else 1, rows, K, dt,
@@ -624,6 +642,8 @@ def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
     if x.dim() < 1:
         raise ValueError("x must have at least 1 dimension")
     *lead, K = x.shape
+    if K > _I32_MAX:
+        _fit(K)
     if x.dim() == 2:
         rows = lead[0]
         stride = _rows(x, "x", dev, rows)
@@ -664,6 +684,8 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
         with _on(dev, stream):
             return mx_dequantize(codes, scales, dtype, out=out)
     K = _mx(codes, scales, "mx", dev)
+    if K > _I32_MAX:
+        _fit(K)
     shape = (*codes.shape[:-1], K)
     if out is None:
         out = codes.new_empty(shape, dtype=dtype)
@@ -698,6 +720,8 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     if w_codes.dim() not in (2, 3):
         raise ValueError(f"w_codes must have 2 or 3 dimensions, got {w_codes.dim()}")
     E, N = (1, w_codes.shape[0]) if w_codes.dim() == 2 else w_codes.shape[:2]
+    if max(E, N, K, top_k) > _I32_MAX or top_k < 0:
+        _fit(E, N, K, top_k)
     offsets = routes = None
     if expert_offsets is not None:
         offsets = _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
