@@ -699,15 +699,19 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
 
 def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
               w_scales: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None, *,
-              sorted_routes: Optional[torch.Tensor] = None, top_k: int = 1,
+              sorted_routes: Optional[torch.Tensor] = None, top_k: Optional[int] = None,
               dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
     """Grouped product of MXFP4 rows with MXFP4 expert weights: out [rows, N] in dtype.
 
     a: [A, K] rows; w: [E, N, K] (or [N, K], one expert); expert_offsets int32 [E+1]: the rows of each
-    expert (may be omitted for one expert).  sorted_routes int32 [rows] (with top_k): row r takes
-    a's row sorted_routes[r] // top_k; without it row r takes a's row r.  Rows behind the last
-    expert's are zero."""
+    expert (may be omitted for one expert).  sorted_routes int32 [rows], only together with top_k: row r
+    takes a's row sorted_routes[r] // top_k (top_k 1: sorted_routes names a's rows); without it row r
+    takes a's row r.  Rows behind the last expert's are zero."""
+    if top_k is None:
+        if sorted_routes is not None:  # permute's routes without their top_k would read other tokens
+            raise ValueError("sorted_routes needs top_k")
+        top_k = 1
     dt = _row_dtype(dtype, "dtype")
     dev = _index(a_codes, "a_codes", 2)
     if _elsewhere(dev, stream):
