@@ -441,7 +441,10 @@ int qmoe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows
  *                      outside [0, a_rows) stands for a row of zeros
  *   top_k              >= 1, used with sorted_routes
  *   out                dtype [rows, N] out (F16, BF16 or F32)
- * Scales of 255 (NaN) make the outputs they enter NaN.  expert_offsets must not
+ * Scales of 255 (NaN) make the outputs they enter NaN.  Scales multiply exactly,
+ * however far apart; terms and sums below float32's normal range (2^-126) may
+ * count as zero, and sums whose terms' magnitudes leave it may be infinite or NaN.
+ * out must not overlap an operand or a table.  expert_offsets must not
  * change while the call runs.  Requires 1 <= E <=
  * 1024, N and K at most 2^20, K a multiple of 32, rows < 2^24, rows * N at
  * most 2^40, and with sorted_routes a_rows * K/2 < 2^31 (else
