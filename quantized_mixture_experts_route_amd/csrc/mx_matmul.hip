@@ -333,9 +333,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     const int K2 = a.K / 2, blocks = a.K / 32;
     // whole groups of steps; with two stages the last may be half a group, but not the only one: the
     // loading side is two steps ahead and would be at its end before the tile begins
-    const int filled = (a.K + 255) / 256;
-    const bool half_group = STAGES == 2 && filled > 2 && (filled - 1) % kGroupSteps < 2;
-    const int steps = (filled + kGroupSteps - 1) / kGroupSteps * kGroupSteps - (half_group ? 2 : 0);
+    const bool half_group = mx_half_group(STAGES, a.K);
+    const int steps = (a.K + 256 * kGroupSteps - 1) / (256 * kGroupSteps) * kGroupSteps - (half_group ? 2 : 0);
 
     // the last stage's space, not loaded before the first barrier, holds the offsets for the first item
     int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
@@ -642,8 +641,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(MxMatmulArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS behind the workgroup's end
 }
 
-constexpr int kCUs = 256;
-
 // wgs_per_cu: as many as fit by LDS and registers.
 template <int DT, int MT, int NT, int WM, int WN, int STAGES>
 hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
@@ -653,56 +650,23 @@ hipError_t launch_tiled(const MxMatmulArgs& a, int wgs_per_cu, hipStream_t s)
     const int64_t experts = a.E < a.rows ? a.E : a.rows;
     const int64_t items = (experts + (a.rows - experts) / BM) * ((a.N + BN - 1) / BN);
     int64_t grid = (items + 7) / 8 * 8;
-    if (grid > kCUs * wgs_per_cu) grid = kCUs * wgs_per_cu;
-    const bool whole = a.K % (STAGES == 2 && a.K > 512 ? 512 : 1024) == 0 && reinterpret_cast<uintptr_t>(a.a_scales) % 16 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.w_scales) % 16 == 0;
-    if (whole) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
+    if (grid > kMxCUs * wgs_per_cu) grid = kMxCUs * wgs_per_cu;
+    if (mx_whole(STAGES, a.K, a.a_scales, a.w_scales)) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
     else launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), dim3(64 * WM * WN), s, a);
     return hipGetLastError();
 }
 
-// Tile by the mean rows of an expert that has some, by how many tiles that makes
-// for 256 CUs, and in the end by the rounds that they take.  Measured in us,
-// weights out of cache, stages in brackets:
-//                                32x64 [4]  64x128 [4]  64x128 [2]  128x128 [2]
-//   E 1, N 4096, K 14336, rows 64   18.8       30.5        45.4        48.7
-//                        rows 1024  92.3       59.6        53.5        53.7 (43.4 with four stages)
-//   E 1, N 4096, K 4096, rows 256   10.1       11.5        13.3        15.2
-//                        rows 512   15.5       12.2        13.9        15.5
-//   E 8, N 4096, K 4096, rows 256   21.6       17.8        20.5        21.9
-//                        rows 512   30.1       23.7        23.1        27.7
-//                        rows 1024  42.7       34.5        38.2        29.9
-//   E 8, N 2048, K 4096, rows 1024   -         23.6        22.9        20.9 (18.0)
-//   E 8, N 4096, K 2048, rows 128   10.6        -          12.3        13.2
-//                        rows 1024   -          -          22.8        19.0
-//   E 512, N 1536, K 2048, rows 60  20.8        -          21.0        23.9
-//   E 512, N 2048, K 768, rows 512  50.3 [2]    -          49.1        52.9
-// The four-stage forms load up to a tile ahead, so K must make two groups.
-// A round of 256 x 256 (one a CU) takes 1.6 times as long as one of 128 x 128
-// (two a CU), for twice the work; rounds of either, and the time of both:
-//   E 8, N 4096, K 2048:  rows 4096: 2 and 3, 43.0 and 37.2;  rows 8192: 3 and 5, 65.4 and 64.3
-//   E 8, N 8192, K 4096:  rows 2048: 2 and 3, 71.1 and 67.5;  rows 4096: 3 and 5, 99.8 and 115.7
-//   E 1, N 4096, K 4096:  rows 4096: 1 and 2, 40.5 and 43.9;  rows 8192: 2 and 4, 71.5 and 81.2
-//   E 1, N 8192, K 8192:  rows 4096: 2 and 4, 133.5 and 182.1
 template <int DT>
 hipError_t launch_by_shape(const MxMatmulArgs& a, hipStream_t s)
 {
-    const int64_t experts = a.E < a.rows ? a.E : a.rows;
-    const int64_t mean = a.rows / experts;
-    auto tiles = [&](int bm, int bn) {  // of several experts, each one's last tile counts half
-        const int64_t m = experts == 1 ? (a.rows + bm - 1) / bm : a.rows / bm + (experts + 1) / 2;
-        return m * ((a.N + bn - 1) / bn);
-    };
-    const int64_t middle = tiles(128, 128);
-    if (a.K > 1024) {
-        if (mean <= 16 || tiles(32, 64) <= 2 * kCUs) return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
-        if (tiles(64, 128) <= kCUs) return launch_tiled<DT, 1, 2, 2, 2, 4>(a, 1, s);
-        if (mean > 64 && middle <= kCUs) return launch_tiled<DT, 2, 2, 2, 2, 4>(a, 1, s);
+    switch (mx_tile(a.E, a.N, a.K, a.rows)) {
+    case MxTile::k32x64s4: return launch_tiled<DT, 1, 1, 1, 2, 4>(a, 2, s);
+    case MxTile::k64x128s4: return launch_tiled<DT, 1, 2, 2, 2, 4>(a, 1, s);
+    case MxTile::k128x128s4: return launch_tiled<DT, 2, 2, 2, 2, 4>(a, 1, s);
+    case MxTile::k64x128s2: return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
+    case MxTile::k128x128s2: return launch_tiled<DT, 2, 2, 2, 2, 2>(a, 2, s);
+    case MxTile::k256x256s2: break;
     }
-    if (mean <= 64 || middle < kCUs) return launch_tiled<DT, 1, 2, 2, 2, 2>(a, 2, s);
-    const int64_t middle_rounds = (middle + 2 * kCUs - 1) / (2 * kCUs);
-    const int64_t large_rounds = (tiles(256, 256) + kCUs - 1) / kCUs;
-    if (8 * large_rounds > 5 * middle_rounds) return launch_tiled<DT, 2, 2, 2, 2, 2>(a, 2, s);
     return launch_tiled<DT, 2, 4, 4, 2, 2>(a, 1, s);
 }
 

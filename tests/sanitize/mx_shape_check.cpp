@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 
 #include "mx_shape.h"
 
@@ -88,10 +89,27 @@ void check_items()
     }
 }
 
+// Lines "E N K rows": the tile, whether scales take the direct path (aligned), whether a half group ends it.
+void answer_forms()
+{
+    static const char* const names[] = {"32x64s4", "64x128s4", "128x128s4", "64x128s2", "128x128s2", "256x256s2"};
+    int E, N, K, rows;
+    while (std::scanf("%d %d %d %d", &E, &N, &K, &rows) == 4) {
+        const char* name = names[(int)qmoe::mx_tile(E, N, K, rows)];
+        const int stages = name[std::strlen(name) - 1] - '0';
+        std::printf("%s %s %s\n", name, qmoe::mx_whole(stages, K, nullptr, nullptr) ? "direct" : "registers",
+                    qmoe::mx_half_group(stages, K) ? "half" : "full");
+    }
+}
+
 }  // namespace
 
-int main()
+int main(int argc, char**)
 {
+    if (argc > 1) {
+        answer_forms();
+        return 0;
+    }
     check_items();
     check_bytes_left();
     check_scale_rows();

@@ -6,6 +6,7 @@ import subprocess
 import pytest
 
 import quantized_mixture_experts_route_amd as qm
+from tests.test_gpu_mx_forms import FORMS
 from tests.test_host_sanitizers import CLANG, FLAGS, ROOT
 
 CSRC = os.path.join(ROOT, "quantized_mixture_experts_route_amd", "csrc")
@@ -52,3 +53,17 @@ def test_more_outputs_than_items_count_are_refused():
     rc = qm.load_library().qmoe_mx_matmul(fake, fake, 1 << 23, fake, fake, 1, 1 << 20, 32, None, None, 1, 1 << 23, 2,
                                           fake, None)
     assert rc == qm.ERR_UNSUPPORTED and "2^40" in qm.last_error()
+
+
+def test_every_form_has_a_case(checker):
+    lines = "".join(f"{E} {N} {K} {sum(counts)}\n" for _, E, K, N, counts in FORMS)
+    res = subprocess.run([checker, "forms"], input=lines, capture_output=True, text=True, timeout=60)
+    assert res.returncode == 0, res.stderr
+    assert res.stdout.splitlines() == [f[0] for f in FORMS]
+    tiles = ["32x64s4", "64x128s4", "128x128s4"]
+    want = {f"{t} {p} full" for t in tiles for p in ("direct", "registers")}
+    want |= {f"{t} {p} {h}" for t in ("64x128s2", "128x128s2", "256x256s2") for p in ("direct", "registers")
+             for h in ("full", "half")}
+    assert {f[0] for f in FORMS} == want
+    # 16-bit rows that start between two words take stores of their own: an odd width for every tile
+    assert {f[0].split()[0] for f in FORMS if f[3] % 2} == {w.split()[0] for w in want}
