@@ -297,6 +297,7 @@ __global__ __launch_bounds__(64 * kScanParts) void scan_kernel(int32_t* __restri
 // Threads that share one token: a power of two, so that a workgroup of 256
 // holds whole tokens and no division splits its index.
 constexpr int kBackThreads = 256;
+constexpr unsigned kBackCUs = 256;
 template <int V>
 int threads_per_token(int H)
 {
@@ -526,10 +527,21 @@ hipError_t unpermute_backward_as(const UnpermuteArgs& a, hipStream_t s)
         launch(kernel, grid, dim3(kBackThreads), s, a.grad_out, a.grad_stride, a.rows, a.row_stride,
                a.route_rows, a.weights, a.T, a.top_k, a.H, log2_of(tpt), a.grad_rows, a.grad_weights);
     };
-    // two rows at a time where there are no more, or few tokens and latency counts; else one:
-    // 4096 tokens of 2048 bf16 columns, top-8 64.7 against 72.3 us, 1023 of 1001, top-6 12.2 against 10.1
-    if (a.top_k <= 2 || a.T < 2048) go(unpermute_backward_kernel<DT, V, 2>);
-    else go(unpermute_backward_kernel<DT, V, 1>);
+    // Two slots at a time, so that their loads overlap.  The bfloat16 form holds 76 registers a lane for
+    // that, six workgroups a CU: where more are launched than fit the chip at once, one slot at a time (56
+    // registers, all eight) is faster.  us, one against two, out of cache:
+    //   bf16, H 2048, top-6: 1024 tokens 20.9, 18.8;  1536 24.0, 22.2;  1792 25.5, 30.9;  4096 50.8, 55.6
+    //         H 4096, top-2: 1024 13.5, 12.6;  1536 15.9, 15.0;  1792 17.6, 20.5;  4096 36.5, 38.2
+    //         H 1001, top-6 (two tokens a workgroup): 2816 26.2, 22.9;  3584 28.6, 32.6
+    //   f16, H 2048, top-4: 1024 14.3, 12.2;  4096 34.8, 32.5
+    //   f32, H 2048, top-4: 512 17.3, 13.0;  2048 34.8, 30.0;  8192 131.8, 129.9
+    if constexpr (DT == kBF16 && V > 1) {
+        if (grid.x > 6 * kBackCUs) {
+            go(unpermute_backward_kernel<DT, V, 1>);
+            return hipGetLastError();
+        }
+    }
+    go(unpermute_backward_kernel<DT, V, 2>);
     return hipGetLastError();
 }
 
