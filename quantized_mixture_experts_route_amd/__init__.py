@@ -425,8 +425,7 @@ def raw_codes(proj: Projection, E: int, N: int, K: int, block_size: int, dtype: 
 
 
 # ------------------------------------------------ sorted by expert and back, MXFP4
-# None of these is recorded by autograd: the gradients are calls of their own (permute_backward,
-# unpermute_backward, mx_matmul on weights quantised with transpose=True).  One call takes a few
+# None of these is recorded by autograd: the gradients are calls of their own.  One call takes a few
 # microseconds on the GPU, so the binding's own time counts: a tensor that is right passes one
 # comparison, and the message is worked out only for one that is not.
 _ROW_DTYPES = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
@@ -526,7 +525,8 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
 
     hidden: float16, bfloat16 or float32 [T, H], any row stride; None: rows is None and only the
     maps are made.  Ids outside [0, E) drop their route: its row, behind the last expert's, is zero
-    and its route_rows entry is -1 - row."""
+    and its route_rows entry is -1 - row.  Autograd does not record the call: rows are detached from
+    hidden, and permute_backward is its gradient."""
     dev = _index(topk_ids, "topk_ids", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -558,7 +558,8 @@ def permute(hidden: Optional[torch.Tensor], topk_ids: torch.Tensor, E: int, *,
 def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows back to their tokens: out[t] = sum over slots of weights[t, s] * rows[route_rows[t, s]]
-    (float32 sums, rounded once; no weights: 1); dropped routes add nothing."""
+    (float32 sums, rounded once; no weights: 1); dropped routes add nothing.  out must not overlap
+    rows.  Autograd does not record the call: unpermute_backward is its gradient."""
     dev = _index(route_rows, "route_rows", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -589,7 +590,10 @@ def permute_backward(grad_rows: torch.Tensor, route_rows: torch.Tensor, *,
 def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], route_rows: torch.Tensor,
                        weights: Optional[torch.Tensor] = None, *, stream=None):
     """The gradient of unpermute: (grad_rows [T*k, H], grad_weights float32 [T, k]).  rows None:
-    grad_weights is not computed (None), as for an unpermute without weights."""
+    grad_weights is not computed (None), as for an unpermute without weights.  route_rows has to be
+    permute's, which names every row once: of a table of one's own, rows that no entry names come back
+    undefined, and -1 stands for a dropped route at row 0, which it clears.  Autograd does not record
+    the call."""
     dev = _index(route_rows, "route_rows", 2)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -619,7 +623,8 @@ def unpermute_backward(grad_out: torch.Tensor, rows: Optional[torch.Tensor], rou
 def mx_quantize(x: torch.Tensor, *, transpose: bool = False, stream=None):
     """MXFP4 codes (uint8 [..., K/2]) and scales (uint8 [..., K/32]) of x [..., K], blocks of 32 along
     K (a matrix may have any row stride).  transpose: x [E, rows, K] or [rows, K] is quantised along
-    its rows, giving codes [E, K, rows/2] and scales [E, K, rows/32] of the transposed matrices."""
+    its rows, giving codes [E, K, rows/2] and scales [E, K, rows/32] of the transposed matrices.
+    Autograd does not record the call (the usual gradient passes straight through)."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x must be a CUDA (HIP) tensor")
     dev = x.get_device()
@@ -707,7 +712,9 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     a: [A, K] rows; w: [E, N, K] (or [N, K], one expert); expert_offsets int32 [E+1]: the rows of each
     expert (may be omitted for one expert).  sorted_routes int32 [rows], only together with top_k: row r
     takes a's row sorted_routes[r] // top_k (top_k 1: sorted_routes names a's rows); without it row r
-    takes a's row r.  Rows behind the last expert's are zero."""
+    takes a's row r.  Rows behind the last expert's are zero.  out must not overlap an operand.  Autograd
+    does not record the call: the gradient of the rows is the same product on w quantised with
+    transpose=True (sorted rows then go through permute_backward to their tokens)."""
     if top_k is None:
         if sorted_routes is not None:  # permute's routes without their top_k would read other tokens
             raise ValueError("sorted_routes needs top_k")
