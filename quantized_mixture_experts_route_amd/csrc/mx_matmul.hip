@@ -59,15 +59,17 @@ __device__ inline i32x8 operand(u32x4 v)
 // LDS too and no step has a tail.  Otherwise scales go through registers, and
 // codes behind the row's end are read out of the buffer's bounds, which gives 0.
 //
-// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 559 us, 3.4
-// PFLOP/s, 1.1 million cycles with the matrix units busy 43% of them, at about
-// 2.0 GHz: power holds the clock down, and a step that took out a sixth of the
-// cycles gained 4% of the time.  Matrix instructions alone would take 354 us (at
-// 1.8 GHz), loads alone 325 us (64 KB a step and CU; 180 us where all of it is
-// in L2), and storing 470 MB adds 100 us: the three overlap in part, since one
-// workgroup fills a CU.  8192^3, one expert: 246 us, 4.5 PFLOP/s.  Rows that
-// do not start on lines cost more: K = 4064 at N 16384, 8192 rows 370 us, K =
-// 4096 303.  Few rows: HBM; 60 rows over 512 experts 21 us for 96 MB (4.6 TB/s).
+// What bounds it.  8192 x 28672 x 4096 over 8 skewed experts: 572 to 583 us on
+// its own (3.3 PFLOP/s), 610 us on average over longer runs, where the card's
+// clock moves a launch between 570 and 757 us.  1.15 million cycles, the matrix
+// units busy in 41% of them, at about 2.0 GHz; an earlier step that took out a
+// sixth of the cycles gained 4% of the time, so power has a part in it.  So has
+// memory: 991 MB are read where the operands hold 508, with 472 MB written 290 us
+// of traffic.  Why the second half is read has not been found.  8192^3, one
+// expert: 266 us, 4.1 PFLOP/s.  Rows that do not start on lines cost more: K =
+// 4064 at N 16384, 8192 rows 370 to 380 us, K = 4096 303.  Short K leaves the
+// stores uncovered: 8192 x 8192 x 1536 over 8 experts 95 us, 2.5 times the floor.
+// Few rows: HBM; 60 rows over 512 experts 22 us for 97 MB (4.4 TB/s).
 constexpr int kStepBytes = 128;  // codes of one row and step
 constexpr int kGroupSteps = 4;   // steps whose scales are loaded together
 constexpr int kScaleBytes = 32;  // ... and their bytes a row

@@ -41,8 +41,10 @@ enum class MxTile { k32x64s4, k64x128s4, k128x128s4, k64x128s2, k128x128s2, k256
 // Tile by the rows an expert gets if all of them (or, of fewer rows, one a row)
 // share alike, by how many tiles that makes for 256 CUs, and in the end by the
 // rounds that they take.  The host knows the offsets' sizes only, so routes that
-// meet in a few of many experts get the tile of an even spread.  Measured in us,
-// weights out of cache, stages in brackets:
+// meet in a few of many experts get the tile of an even spread: 8192 rows all on
+// 4 of 512 experts, N 4096, K 2048 take 126 us, on 4 of 128 experts 63, and with
+// those 4 experts alone 49.  Measured in us, weights out of cache, stages in
+// brackets:
 //                                32x64 [4]  64x128 [4]  64x128 [2]  128x128 [2]
 //   E 1, N 4096, K 14336, rows 64   18.8       30.5        45.4        48.7
 //                        rows 1024  92.3       59.6        53.5        53.7 (43.4 with four stages)

@@ -23,9 +23,10 @@
 // weights.  The gradient of the weighted sum is w * grad_out at the route's
 // row and, for the weight, the dot product of grad_out with that row.  All of
 // them move each row once and do a few operations an element, so they are
-// bound by HBM: 4096 tokens of 4096 bf16 columns, top-2, take 22 us to sort
-// (100 MB, 4.6 TB/s), 19 us to bring back (5.2 TB/s) and 34 us for the
-// gradient (168 MB, 4.9 TB/s), inputs out of cache.
+// bound by HBM: 4096 tokens of 4096 bf16 columns, top-2, take 30 us to sort
+// (100 MB, 3.4 TB/s), 21 us to bring back (4.9 TB/s) and 34 us for the
+// gradient (168 MB, 4.9 TB/s) with inputs out of cache; 23, 17 and 31 us with
+// the inputs of the pass before.
 #include "expert_ops.h"
 #include "qmoe_internal.h"
 #include "rowio.h"
@@ -535,6 +536,9 @@ hipError_t unpermute_backward_as(const UnpermuteArgs& a, hipStream_t s)
     //         H 1001, top-6 (two tokens a workgroup): 2816 26.2, 22.9;  3584 28.6, 32.6
     //   f16, H 2048, top-4: 1024 14.3, 12.2;  4096 34.8, 32.5
     //   f32, H 2048, top-4: 512 17.3, 13.0;  2048 34.8, 30.0;  8192 131.8, 129.9
+    // Inputs that are still in cache like two slots better between 3500 and 6100 tokens of H 4096 (top-2
+    // 4096 tokens: 36.0, 33.7); there the rule goes by what a training step meets.  A bound of 64 registers
+    // on the bfloat16 form spills and loses everywhere.
     if constexpr (DT == kBF16 && V > 1) {
         if (grid.x > 6 * kBackCUs) {
             go(unpermute_backward_kernel<DT, V, 1>);
