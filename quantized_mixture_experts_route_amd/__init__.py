@@ -475,6 +475,20 @@ def _rows(t, name: str, index: int, n: int) -> int:
     return stride if n > 1 else h
 
 
+def _end(t: torch.Tensor) -> int:
+    """The address behind a tensor's last element."""
+    return t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+
+
+def _apart(out: torch.Tensor, **inputs) -> None:
+    """Checks that a given output shares no memory with what its kernel reads meanwhile."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for name, t in inputs.items():
+        if t is not None and t.numel() and lo < _end(t) and t.data_ptr() < hi:
+            raise ValueError(f"out overlaps {name}")
+
+
 _I32_MAX = (1 << 31) - 1
 
 
@@ -577,6 +591,7 @@ def unpermute(rows: torch.Tensor, route_rows: torch.Tensor, weights: Optional[to
         to = out.data_ptr()
     else:
         to = _tensor(out, "out", dev, rows.dtype, (T, H))
+        _apart(out, rows=rows, route_rows=route_rows, weights=weights)
     _check(load_library().qmoe_unpermute(rows.data_ptr(), stride, at, w, T, top_k, H, dt, to, _current(dev)))
     return out
 
@@ -697,6 +712,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype,
         to = out.data_ptr()
     else:
         to = _tensor(out, "out", dev, dtype, shape)
+        _apart(out, codes=codes, scales=scales)
     _check(load_library().qmoe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), math.prod(shape[:-1]), K, dt,
                                              to, _current(dev)))
     return out
@@ -746,6 +762,8 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
         to = out.data_ptr()
     else:
         to = _tensor(out, "out", dev, dtype, (rows, N))
+        _apart(out, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales,
+               expert_offsets=expert_offsets, sorted_routes=sorted_routes)
     _check(load_library().qmoe_mx_matmul(
         a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
         routes, top_k, rows, dt, to, _current(dev)))
