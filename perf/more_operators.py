@@ -117,7 +117,8 @@ def draw(rng):
     T = _log(rng, 1, 8192)
     while T > 1 and T * k * N * K > 1 << 39:
         T //= 2
-    return dict(op=op, T=T, k=k, E=E, K=K, N=N, dtype=dtype, gather=rng.random() < 0.7,
+    # 16-bit outputs: sums of 8-bit products on matrix units are not float32's
+    return dict(op=op, T=T, k=k, E=E, K=K, N=N, dtype=rng.choice(["f16", "bf16"]), gather=rng.random() < 0.7,
                 skew=rng.choice([0.0, 0.0, 2.0]), scales=rng.choice(["two", "any"]))
 
 
