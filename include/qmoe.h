@@ -51,7 +51,7 @@ extern "C" {
 /* activation dtypes (hidden states, scales, output) */
 #define QMOE_DTYPE_F16 1
 #define QMOE_DTYPE_BF16 2
-#define QMOE_DTYPE_F32 3 /* rows of the sort by expert and of the MXFP4 operators only */
+#define QMOE_DTYPE_F32 3 /* the operators beside the layer only (from qmoe_permute on) */
 
 /* gated activations on interleaved fc1 rows (row 2j = gate, 2j+1 = up)
  * [qmoe.rs, qmoe_activate with swiglu_fusion = 1; PR 32198, GeGLU uses the same
@@ -455,6 +455,140 @@ int qmoe_mx_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_ro
                    const uint8_t* w_codes, const uint8_t* w_scales, int32_t E, int32_t N,
                    int32_t K, const int32_t* expert_offsets, const int32_t* sorted_routes,
                    int32_t top_k, int64_t rows, int32_t dtype, void* out, void* stream);
+
+/*
+ * Routing by scores: the experts of each token by softmax or sigmoid scores,
+ * with a bias for balance and with groups of experts.
+ *   logits      dtype [T, E] (F16, BF16 or F32), rows row_stride elements
+ *               apart, aligned to its element
+ *   bias        NULL, or float32 [E]: added to the scores where experts are
+ *               chosen, not to the weights
+ *   score       QMOE_SCORE_SOFTMAX (over all E) or QMOE_SCORE_SIGMOID
+ *   n_groups    experts come in n_groups groups of E / n_groups neighbours;
+ *               a token chooses from its top_groups best groups only
+ *   group_top   1 or 2: a group's rank is the sum of its 1 or 2 best choices
+ *   normalize   nonzero: a token's weights are divided by their sum
+ *   scale       the weights' factor
+ *   ids         int32 [T, top_k] out, best choice first
+ *   weights     float32 [T, top_k] out
+ * choice = score + bias; choices and group ranks are compared as float64
+ * values, ties go to the lower index.  An expert whose logit or choice is -inf
+ * is masked: it is never chosen, and takes no part in a group's rank.  Slots
+ * without an expert left get the id -1 and the weight 0, so qmoe_permute drops
+ * them; a row of -inf alone makes all of a token's slots such.  A NaN choice
+ * ranks above all.  A sigmoid of NaN makes its weight NaN (with normalize, the
+ * row's); a NaN, or a +inf under softmax, makes the weights of its row NaN and
+ * its choice of experts unspecified (distinct ids in range).
+ * Requires 1 <= E <= 1024, 1 <= top_k <= 64 (else QMOE_ERR_UNSUPPORTED) and at
+ * most E / n_groups * top_groups, n_groups <= 64 and a divisor of E, 1 <=
+ * top_groups <= n_groups, T < 2^23, a finite scale.  T = 0 returns QMOE_OK and
+ * enqueues nothing.
+ *
+ * qmoe_route_scores_backward: the gradient of the weights with respect to the
+ * logits (the choice itself has none).
+ *   grad_weights  float32 [T, top_k]
+ *   ids           int32 [T, top_k] as qmoe_route_scores wrote it; a slot whose
+ *                 id is outside [0, E) or whose expert's logit is -inf adds nothing
+ *   grad_logits   dtype [T, E] out, dense, every element written, float32 sums
+ *                 rounded once; must not overlap an input
+ * score, normalize and scale as in the forward call.
+ */
+#define QMOE_SCORE_SOFTMAX 0
+#define QMOE_SCORE_SIGMOID 1
+int qmoe_route_scores(const void* logits, int64_t row_stride, int64_t T, int32_t E, int32_t dtype,
+                      const float* bias, int32_t top_k, int32_t score, int32_t n_groups,
+                      int32_t top_groups, int32_t group_top, int32_t normalize, float scale,
+                      int32_t* ids, float* weights, void* stream);
+int qmoe_route_scores_backward(const float* grad_weights, const void* logits, int64_t row_stride,
+                               const int32_t* ids, int64_t T, int32_t E, int32_t dtype,
+                               int32_t top_k, int32_t score, int32_t normalize, float scale,
+                               void* grad_logits, void* stream);
+
+/*
+ * 8-bit floating point with a float32 scale for each block of 128: codes are
+ * e4m3 bytes (the Open Compute Project's 8-bit formats: largest value 448, no
+ * infinities, 0x7f and 0xff are NaN), a value is code * scale.  codes are
+ * 16-byte aligned, and their last axis is a multiple of 16 (else
+ * QMOE_ERR_UNSUPPORTED); a last block may be short.
+ *
+ * qmoe_blocks_quantize: x dtype [rows, K], rows row_stride elements apart, to
+ * codes [rows, K] and scales [rows, ceil(K/128)].  A block's scale is the least
+ * power of two, at least 2^-126, that holds its largest magnitude within 448;
+ * codes are x / scale (an exact quotient) rounded to nearest, ties to even.  A
+ * zero block has the scale 2^-126; a block with a NaN or an infinity has the
+ * scale NaN and codes 0.  rows*K <= 2^34.
+ *
+ * qmoe_blocks_quantize_weights: x dtype [E, rows, K] dense, in squares of 128 x
+ * 128, to codes [E, rows, K] and scales [E, ceil(rows/128), ceil(K/128)]; with
+ * transpose, to those of the transposed matrices: codes [E, K, rows] (rows a
+ * multiple of 16, any K) and scales [E, ceil(K/128), ceil(rows/128)], the same
+ * codes and scales at their transposed places.
+ *
+ * qmoe_blocks_dequantize, qmoe_blocks_dequantize_weights: the values, code * scale in
+ * float32, rounded to dtype; scales may be any float32 values (a checkpoint's).
+ */
+int qmoe_blocks_quantize(const void* x, int64_t row_stride, int64_t rows, int32_t K, int32_t dtype,
+                      uint8_t* codes, float* scales, void* stream);
+int qmoe_blocks_quantize_weights(const void* x, int32_t E, int32_t rows, int32_t K, int32_t dtype,
+                              int32_t transpose, uint8_t* codes, float* scales, void* stream);
+int qmoe_blocks_dequantize(const uint8_t* codes, const float* scales, int64_t rows, int32_t K,
+                        int32_t dtype, void* out, void* stream);
+int qmoe_blocks_dequantize_weights(const uint8_t* codes, const float* scales, int32_t E, int32_t rows,
+                                int32_t K, int32_t dtype, void* out, void* stream);
+
+/*
+ * Grouped product of such rows with such expert weights, one launch:
+ *   out[r, n] = sum over blocks b of sa[src(r), b] * sw[e(r), n/128, b] *
+ *               sum over k in b of a[src(r), k] * w[e(r), n, k]
+ * dtype is F16 or BF16.  The matrix instruction adds each eight neighbouring
+ * products to 2^-13 of their largest, and those sums in float32; on values as
+ * tokens and weights have them the result is good to 2^-15 or better, which is
+ * below the rounding to 16 bits but not float32's precision: F32 is refused.
+ *   a_codes, a_scales  [a_rows, K], float32 [a_rows, ceil(K/128)]
+ *   w_codes, w_scales  [E, N, K], float32 [E, ceil(N/128), ceil(K/128)]
+ *   expert_offsets, sorted_routes, top_k, rows, out   as in qmoe_mx_matmul
+ * The scales may be any float32 values; the product of two is rounded to
+ * float32, so it must stay in float32's range (below 2^-126 it may count as 0).
+ * A NaN scale or code makes the outputs it enters NaN.  With sorted_routes
+ * a_rows * K < 2^31; dtype F16 or BF16, N and K at most 2^20, K a multiple of 16, E <= 1024, rows
+ * < 2^24, rows * N at most 2^40 (else QMOE_ERR_UNSUPPORTED).  rows = 0 returns
+ * QMOE_OK and enqueues nothing.
+ */
+int qmoe_blocks_matmul(const uint8_t* a_codes, const float* a_scales, int64_t a_rows,
+                    const uint8_t* w_codes, const float* w_scales, int32_t E, int32_t N, int32_t K,
+                    const int32_t* expert_offsets, const int32_t* sorted_routes, int32_t top_k,
+                    int64_t rows, int32_t dtype, void* out, void* stream);
+
+/*
+ * The gated activation of a projection's outputs, as the layer's kernels fuse it.
+ *   y        dtype [rows, 2*I] (F16, BF16 or F32), rows row_stride elements apart
+ *   activation, activation_alpha, activation_beta, swiglu_limit   as in
+ *            qmoe_layer_opts, except that a NaN gate makes its output NaN
+ *   swiglu_fusion  QMOE_SWIGLU_INTERLEAVED (gate 2j, up 2j+1) or
+ *            QMOE_SWIGLU_HALVES (gate j, up I + j), of either activation
+ * qmoe_activate: out dtype [rows, I], float32 arithmetic rounded once.
+ * qmoe_activate_blocks: the float32 values straight to the codes [rows, I] and
+ * scales [rows, ceil(I/128)] of qmoe_blocks_quantize (I a multiple of 16, else
+ * QMOE_ERR_UNSUPPORTED).
+ * qmoe_activate_backward: grad dtype [rows, I], rows grad_stride elements
+ * apart, the gradient of the activation's output; grad_y dtype [rows, 2*I] out,
+ * the gradient of y.  Where a limit cuts a value, its gradient is 0 (at the limit
+ * itself it passes).
+ * Outputs are dense and must not overlap the inputs.  Requires 1 <= I <= 2^19,
+ * rows*I <= 2^34, no NaN among the parameters, swiglu_limit > 0.  rows = 0
+ * returns QMOE_OK and enqueues nothing.
+ */
+int qmoe_activate(const void* y, int64_t row_stride, int64_t rows, int32_t I, int32_t dtype,
+                  int32_t activation, int32_t swiglu_fusion, float activation_alpha,
+                  float activation_beta, float swiglu_limit, void* out, void* stream);
+int qmoe_activate_blocks(const void* y, int64_t row_stride, int64_t rows, int32_t I, int32_t dtype,
+                      int32_t activation, int32_t swiglu_fusion, float activation_alpha,
+                      float activation_beta, float swiglu_limit, uint8_t* codes, float* scales,
+                      void* stream);
+int qmoe_activate_backward(const void* grad, int64_t grad_stride, const void* y, int64_t row_stride,
+                           int64_t rows, int32_t I, int32_t dtype, int32_t activation,
+                           int32_t swiglu_fusion, float activation_alpha, float activation_beta,
+                           float swiglu_limit, void* grad_y, void* stream);
 
 /*
  * Test hook: the dequantization of the weight-rounding kernels, written out

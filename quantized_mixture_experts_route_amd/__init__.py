@@ -42,7 +42,10 @@ EXPORTED = ("qmoe_last_error", "qmoe_route", "qmoe_router", "qmoe_worklist_capac
             "qmoe_shared_workspace_size", "qmoe_forward_shared", "qmoe_dequantize",
             "qmoe_raw_codes", "qmoe_permute_workspace_size", "qmoe_permute", "qmoe_unpermute",
             "qmoe_unpermute_backward", "qmoe_mx_quantize", "qmoe_mx_quantize_columns",
-            "qmoe_mx_dequantize", "qmoe_mx_matmul",
+            "qmoe_mx_dequantize", "qmoe_mx_matmul", "qmoe_route_scores", "qmoe_route_scores_backward",
+            "qmoe_blocks_quantize", "qmoe_blocks_quantize_weights", "qmoe_blocks_dequantize",
+            "qmoe_blocks_dequantize_weights", "qmoe_blocks_matmul", "qmoe_activate", "qmoe_activate_blocks",
+            "qmoe_activate_backward",
             "qmoe_timer_start", "qmoe_timer_stop")
 
 
@@ -66,6 +69,9 @@ class _LayerOpts(ctypes.Structure):
 
 
 SWIGLU_SEPARATE, SWIGLU_INTERLEAVED, SWIGLU_HALVES = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+FP8_BLOCK = 128
+FP8_DTYPE = torch.float8_e4m3fn
 
 
 _lib = None
@@ -117,6 +123,16 @@ def load_library(path: str = LIB_PATH):
     lib.qmoe_mx_quantize_columns.argtypes = [P, i32, i32, i32, i32, P, P, P]
     lib.qmoe_mx_dequantize.argtypes = [P, P, i64, i32, i32, P, P]
     lib.qmoe_mx_matmul.argtypes = [P, P, i64, P, P, i32, i32, i32, P, P, i32, i64, i32, P, P]
+    lib.qmoe_route_scores.argtypes = [P, i64, i64, i32, i32, P, i32, i32, i32, i32, i32, i32, f32, P, P, P]
+    lib.qmoe_route_scores_backward.argtypes = [P, P, i64, P, i64, i32, i32, i32, i32, i32, f32, P, P]
+    lib.qmoe_blocks_quantize.argtypes = [P, i64, i64, i32, i32, P, P, P]
+    lib.qmoe_blocks_quantize_weights.argtypes = [P, i32, i32, i32, i32, i32, P, P, P]
+    lib.qmoe_blocks_dequantize.argtypes = [P, P, i64, i32, i32, P, P]
+    lib.qmoe_blocks_dequantize_weights.argtypes = [P, P, i32, i32, i32, i32, P, P]
+    lib.qmoe_blocks_matmul.argtypes = [P, P, i64, P, P, i32, i32, i32, P, P, i32, i64, i32, P, P]
+    lib.qmoe_activate.argtypes = [P, i64, i64, i32, i32, i32, i32, f32, f32, f32, P, P]
+    lib.qmoe_activate_blocks.argtypes = [P, i64, i64, i32, i32, i32, i32, f32, f32, f32, P, P, P]
+    lib.qmoe_activate_backward.argtypes = [P, i64, P, i64, i64, i32, i32, i32, i32, f32, f32, f32, P, P]
     lib.qmoe_timer_start.argtypes = [i32]
     lib.qmoe_timer_stop.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
     for name in ("qmoe_route", "qmoe_router", "qmoe_group", "qmoe_forward", "qmoe_forward_ex",
@@ -124,7 +140,10 @@ def load_library(path: str = LIB_PATH):
                  "qmoe_forward_shared",
                  "qmoe_dequantize", "qmoe_raw_codes", "qmoe_permute", "qmoe_unpermute",
                  "qmoe_unpermute_backward", "qmoe_mx_quantize", "qmoe_mx_quantize_columns",
-                 "qmoe_mx_dequantize", "qmoe_mx_matmul",
+                 "qmoe_mx_dequantize", "qmoe_mx_matmul", "qmoe_route_scores",
+                 "qmoe_route_scores_backward", "qmoe_blocks_quantize", "qmoe_blocks_quantize_weights",
+                 "qmoe_blocks_dequantize", "qmoe_blocks_dequantize_weights", "qmoe_blocks_matmul",
+                 "qmoe_activate", "qmoe_activate_blocks", "qmoe_activate_backward",
                  "qmoe_timer_start", "qmoe_timer_stop"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -767,6 +786,321 @@ def mx_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tens
     _check(load_library().qmoe_mx_matmul(
         a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
         routes, top_k, rows, dt, to, _current(dev)))
+    return out
+
+
+# ------------------------------------------------ routing by scores, 8-bit floating point, gated activation
+# As above: autograd records none of these, and the gradients are calls of their own.
+def route_scores(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMAX,
+                 bias: Optional[torch.Tensor] = None, n_groups: int = 1, top_groups: Optional[int] = None,
+                 group_top: int = 1, normalize: bool = True, scale: float = 1.0, stream=None):
+    """Experts of each token by scores: (ids int32 [T, k], weights float32 [T, k]).
+
+    logits: float16, bfloat16 or float32 [T, E], any row stride.  score: SCORE_SOFTMAX or SCORE_SIGMOID.
+    bias float32 [E] is added to the scores for the choice alone.  Experts come in n_groups groups of
+    neighbours, ranked by the sum of their group_top (1 or 2) best choices; the top_groups best (all, if
+    not given) take part.  Choices are compared in float64, ties go to the lower index.  normalize divides
+    a token's weights by their sum; scale multiplies them.  An expert with a logit of -inf is never
+    chosen; slots without an expert left have the id -1 and the weight 0, which permute drops.  Autograd
+    does not record the call: route_scores_backward is its gradient."""
+    dev = _index(logits, "logits", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return route_scores(logits, top_k, score=score, bias=bias, n_groups=n_groups, top_groups=top_groups,
+                                group_top=group_top, normalize=normalize, scale=scale)
+    T, E = logits.shape
+    stride, dt = _rows(logits, "logits", dev, T), _row_dtype(logits.dtype, "logits")
+    if top_groups is None:
+        top_groups = n_groups
+    _fit(E, top_k, score, n_groups, top_groups, group_top)
+    b = None if bias is None else _tensor(bias, "bias", dev, torch.float32, (E,))
+    ids = logits.new_empty((T, max(top_k, 0)), dtype=torch.int32)
+    weights = logits.new_empty((T, max(top_k, 0)), dtype=torch.float32)
+    _check(load_library().qmoe_route_scores(
+        logits.data_ptr(), stride, T, E, dt, b, top_k, score, n_groups, top_groups, group_top, bool(normalize),
+        scale, ids.data_ptr(), weights.data_ptr(), _current(dev)))
+    return ids, weights
+
+
+def route_scores_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, *,
+                          score: int = SCORE_SOFTMAX, normalize: bool = True, scale: float = 1.0,
+                          stream=None) -> torch.Tensor:
+    """The gradient of route_scores' weights with respect to the logits, [T, E] in their dtype.
+    grad_weights float32 [T, k]; ids as route_scores returned them (a slot of -1 adds nothing); score,
+    normalize and scale as there."""
+    dev = _index(logits, "logits", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return route_scores_backward(grad_weights, logits, ids, score=score, normalize=normalize, scale=scale)
+    T, E = logits.shape
+    stride, dt = _rows(logits, "logits", dev, T), _row_dtype(logits.dtype, "logits")
+    _index(ids, "ids", 2)
+    shape = ids.shape
+    if shape[0] != T:
+        raise ValueError(f"ids has shape {tuple(shape)}, expected {T} rows")
+    at = _tensor(ids, "ids", dev, torch.int32, shape)
+    g = _tensor(grad_weights, "grad_weights", dev, torch.float32, shape)
+    _fit(E, shape[1], score)
+    out = logits.new_empty((T, E))
+    _check(load_library().qmoe_route_scores_backward(g, logits.data_ptr(), stride, at, T, E, dt, shape[1], score,
+                                                     bool(normalize), scale, out.data_ptr(), _current(dev)))
+    return out
+
+
+def _fp8_blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def fp8_quantize(x: torch.Tensor, *, stream=None):
+    """e4m3 codes (float8_e4m3fn [..., K]) and scales (float32 [..., K/128 rounded up]) of x [..., K], one
+    scale for each 128 values of a row (a matrix may have any row stride); K a multiple of 16.  A scale is
+    the least power of two that holds its block within 448.  Autograd does not record the call (the usual
+    gradient passes straight through)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA (HIP) tensor")
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fp8_quantize(x)
+    dt = _row_dtype(x.dtype, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least 1 dimension")
+    *lead, K = x.shape
+    if K > _I32_MAX:
+        _fit(K)
+    if x.dim() == 2:
+        rows = lead[0]
+        stride = _rows(x, "x", dev, rows)
+    else:
+        _dev(x, "x")
+        rows, stride = math.prod(lead), K
+    codes = x.new_empty((*lead, K), dtype=FP8_DTYPE)
+    scales = x.new_empty((*lead, _fp8_blocks(K)), dtype=torch.float32)
+    _check(load_library().qmoe_blocks_quantize(x.data_ptr(), stride, rows, K, dt, codes.data_ptr(), scales.data_ptr(),
+                                            _current(dev)))
+    return codes, scales
+
+
+def fp8_quantize_weights(w: torch.Tensor, *, transpose: bool = False, stream=None):
+    """e4m3 codes and float32 scales of w [E, N, K] or [N, K], one scale for each square of 128 x 128:
+    codes [E, N, K] and scales [E, N/128, K/128 rounded up] (K a multiple of 16).  transpose: the same codes
+    and scales at their transposed places, [E, K, N] and [E, K/128, N/128] (N a multiple of 16, any K), which
+    the gradient's product takes."""
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise ValueError("w must be a CUDA (HIP) tensor")
+    dev = w.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fp8_quantize_weights(w, transpose=transpose)
+    dt = _row_dtype(w.dtype, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must have 2 or 3 dimensions, got {w.dim()}")
+    _dev(w, "w")
+    *lead, N, K = w.shape
+    E = lead[0] if lead else 1
+    _fit(E, N, K)
+    R, C = (K, N) if transpose else (N, K)
+    codes = w.new_empty((*lead, R, C), dtype=FP8_DTYPE)
+    scales = w.new_empty((*lead, _fp8_blocks(R), _fp8_blocks(C)), dtype=torch.float32)
+    _check(load_library().qmoe_blocks_quantize_weights(w.data_ptr(), E, N, K, dt, bool(transpose), codes.data_ptr(),
+                                                    scales.data_ptr(), _current(dev)))
+    return codes, scales
+
+
+def _fp8(codes, scales, name: str, index: int, square: bool):
+    """Checks a pair of codes [..., R, K] and scales [..., R or R/128 rounded up, K/128 rounded up]; codes' shape."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() < (2 if square else 1):
+        _dev(codes, f"{name}_codes", FP8_DTYPE)
+        raise ValueError(f"{name}_codes has {codes.dim()} dimensions")
+    shape = codes.shape
+    want = (*shape[:-1], _fp8_blocks(shape[-1]))
+    if square:
+        want = (*shape[:-2], _fp8_blocks(shape[-2]), want[-1])
+    _tensor(codes, f"{name}_codes", index, FP8_DTYPE, shape)
+    _tensor(scales, f"{name}_scales", index, torch.float32, want)
+    return shape
+
+
+def _fp8_device(codes) -> int:
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise ValueError("codes must be a CUDA (HIP) tensor")
+    return codes.get_device()
+
+
+def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype, *,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """What e4m3 codes [..., K] with scales [..., K/128 rounded up] stand for, [..., K] in dtype."""
+    dt = _row_dtype(dtype, "dtype")
+    dev = _fp8_device(codes)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fp8_dequantize(codes, scales, dtype, out=out)
+    shape = _fp8(codes, scales, "fp8", dev, False)
+    K = shape[-1]
+    if K > _I32_MAX:
+        _fit(K)
+    if out is None:
+        out = codes.new_empty(shape, dtype=dtype)
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, dtype, shape)
+        _apart(out, codes=codes, scales=scales)
+    _check(load_library().qmoe_blocks_dequantize(codes.data_ptr(), scales.data_ptr(), math.prod(shape[:-1]), K, dt, to,
+                                              _current(dev)))
+    return out
+
+
+def fp8_dequantize_weights(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype, *,
+                           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """What e4m3 codes [E, N, K] or [N, K] with scales for squares of 128 x 128 stand for, in dtype."""
+    dt = _row_dtype(dtype, "dtype")
+    dev = _fp8_device(codes)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fp8_dequantize_weights(codes, scales, dtype, out=out)
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"codes must have 2 or 3 dimensions, got {codes.dim()}")
+    shape = _fp8(codes, scales, "fp8", dev, True)
+    *lead, N, K = shape
+    E = lead[0] if lead else 1
+    _fit(E, N, K)
+    if out is None:
+        out = codes.new_empty(shape, dtype=dtype)
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, dtype, shape)
+        _apart(out, codes=codes, scales=scales)
+    _check(load_library().qmoe_blocks_dequantize_weights(codes.data_ptr(), scales.data_ptr(), E, N, K, dt, to,
+                                                      _current(dev)))
+    return out
+
+
+def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+               expert_offsets: Optional[torch.Tensor] = None, *, sorted_routes: Optional[torch.Tensor] = None,
+               top_k: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Grouped product of e4m3 rows with e4m3 expert weights, a float32 scale for each block of 128: out
+    [rows, N] in dtype (float16 or bfloat16; the matrix units' sums of 8-bit products are good to 2^-15).
+
+    a: codes [A, K], scales [A, K/128 rounded up] (fp8_quantize); w: codes [E, N, K] (or [N, K], one
+    expert), scales [E, N/128, K/128 rounded up] (fp8_quantize_weights, or a checkpoint's: any float32
+    values).  expert_offsets, sorted_routes, top_k and out as in mx_matmul.  Rows behind the last expert's
+    are zero.  Autograd does not record the call: the gradient of the rows is the same product on w
+    quantised with transpose=True (sorted rows then go through permute_backward to their tokens)."""
+    if top_k is None:
+        if sorted_routes is not None:  # permute's routes without their top_k would read other tokens
+            raise ValueError("sorted_routes needs top_k")
+        top_k = 1
+    dt = _row_dtype(dtype, "dtype")
+    dev = _index(a_codes, "a_codes", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return fp8_matmul(a_codes, a_scales, w_codes, w_scales, expert_offsets, sorted_routes=sorted_routes,
+                              top_k=top_k, dtype=dtype, out=out)
+    A, K = _fp8(a_codes, a_scales, "a", dev, False)
+    shape = _fp8(w_codes, w_scales, "w", dev, True)
+    if len(shape) not in (2, 3):
+        raise ValueError(f"w_codes must have 2 or 3 dimensions, got {len(shape)}")
+    E, N = (1, shape[0]) if len(shape) == 2 else shape[:2]
+    if shape[-1] != K:
+        raise ValueError(f"a has {K} values a row, w {shape[-1]}")
+    if max(E, N, K, top_k) > _I32_MAX or top_k < 0:
+        _fit(E, N, K, top_k)
+    offsets = routes = None
+    if expert_offsets is not None:
+        offsets = _tensor(expert_offsets, "expert_offsets", dev, torch.int32, (E + 1,))
+    rows = A
+    if sorted_routes is not None:
+        _index(sorted_routes, "sorted_routes", 1)
+        rows = sorted_routes.shape[0]
+        routes = _tensor(sorted_routes, "sorted_routes", dev, torch.int32, (rows,))
+    if out is None:
+        out = a_codes.new_empty((rows, N), dtype=dtype)
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, dtype, (rows, N))
+        _apart(out, a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales,
+               expert_offsets=expert_offsets, sorted_routes=sorted_routes)
+    _check(load_library().qmoe_blocks_matmul(
+        a_codes.data_ptr(), a_scales.data_ptr(), A, w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, offsets,
+        routes, top_k, rows, dt, to, _current(dev)))
+    return out
+
+
+def _pairs(y, name: str = "y"):
+    """Device, rows, I, row stride and dtype of y [rows, 2*I]."""
+    dev = _index(y, name, 2)
+    rows, width = y.shape
+    if width % 2:
+        raise ValueError(f"{name} has {width} columns, which are no pairs of gate and up")
+    stride, dt = _rows(y, name, dev, rows), _row_dtype(y.dtype, name)
+    if width > _I32_MAX:
+        _fit(width)
+    return rows, width // 2, stride, dt
+
+
+def activate(y: torch.Tensor, *, activation: int = ACT_SWIGLU, swiglu_fusion: int = SWIGLU_INTERLEAVED,
+             activation_alpha: float = 1.0, activation_beta: float = 0.0, swiglu_limit: float = math.inf,
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gated activation of a projection's outputs y [rows, 2*I] (float16, bfloat16 or float32, any row
+    stride): [rows, I] in y's dtype.  Options as in forward (SWIGLU_INTERLEAVED or SWIGLU_HALVES, of either
+    activation).  Autograd does not record the call: activate_backward is its gradient."""
+    dev = _index(y, "y", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return activate(y, activation=activation, swiglu_fusion=swiglu_fusion, activation_alpha=activation_alpha,
+                            activation_beta=activation_beta, swiglu_limit=swiglu_limit, out=out)
+    rows, I, stride, dt = _pairs(y)
+    if out is None:
+        out = y.new_empty((rows, I))
+        to = out.data_ptr()
+    else:
+        to = _tensor(out, "out", dev, y.dtype, (rows, I))
+        _apart(out, y=y)
+    _check(load_library().qmoe_activate(y.data_ptr(), stride, rows, I, dt, activation, swiglu_fusion,
+                                        activation_alpha, activation_beta, swiglu_limit, to, _current(dev)))
+    return out
+
+
+def activate_fp8(y: torch.Tensor, *, activation: int = ACT_SWIGLU, swiglu_fusion: int = SWIGLU_INTERLEAVED,
+                 activation_alpha: float = 1.0, activation_beta: float = 0.0, swiglu_limit: float = math.inf,
+                 stream=None):
+    """The gated activation straight to 8 bits: codes [rows, I] and scales [rows, I/128 rounded up] as
+    fp8_quantize gives them, of the float32 values (I a multiple of 16).  Arguments as in activate."""
+    dev = _index(y, "y", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return activate_fp8(y, activation=activation, swiglu_fusion=swiglu_fusion,
+                                activation_alpha=activation_alpha, activation_beta=activation_beta,
+                                swiglu_limit=swiglu_limit)
+    rows, I, stride, dt = _pairs(y)
+    codes = y.new_empty((rows, I), dtype=FP8_DTYPE)
+    scales = y.new_empty((rows, _fp8_blocks(I)), dtype=torch.float32)
+    _check(load_library().qmoe_activate_blocks(y.data_ptr(), stride, rows, I, dt, activation, swiglu_fusion,
+                                            activation_alpha, activation_beta, swiglu_limit, codes.data_ptr(),
+                                            scales.data_ptr(), _current(dev)))
+    return codes, scales
+
+
+def activate_backward(grad: torch.Tensor, y: torch.Tensor, *, activation: int = ACT_SWIGLU,
+                      swiglu_fusion: int = SWIGLU_INTERLEAVED, activation_alpha: float = 1.0,
+                      activation_beta: float = 0.0, swiglu_limit: float = math.inf, stream=None) -> torch.Tensor:
+    """The gradient of activate with respect to y, [rows, 2*I]: grad [rows, I] in y's dtype, any row stride.
+    Where swiglu_limit cuts a value its gradient is 0."""
+    dev = _index(y, "y", 2)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return activate_backward(grad, y, activation=activation, swiglu_fusion=swiglu_fusion,
+                                     activation_alpha=activation_alpha, activation_beta=activation_beta,
+                                     swiglu_limit=swiglu_limit)
+    rows, I, stride, dt = _pairs(y)
+    gstride = _rows(grad, "grad", dev, rows)
+    if grad.dtype is not y.dtype or grad.shape[1] != I:
+        raise ValueError(f"grad is {grad.dtype} {tuple(grad.shape)}, expected {y.dtype} {(rows, I)}")
+    out = y.new_empty((rows, 2 * I))
+    _check(load_library().qmoe_activate_backward(grad.data_ptr(), gstride, y.data_ptr(), stride, rows, I, dt,
+                                                 activation, swiglu_fusion, activation_alpha, activation_beta,
+                                                 swiglu_limit, out.data_ptr(), _current(dev)))
     return out
 
 

@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 SOURCES = ["qmoe_api.cpp", "route.hip", "group.hip", "plan.hip", "gemm_prefill.hip", "gemm_decode.hip", "gemm_stream.hip",
            "combine.hip", "dequant.hip", "noalloc.hip", "router.hip", "shared.hip",
-           "expert_ops.cpp", "permute.hip", "mx_convert.hip", "mx_matmul.hip"]
+           "expert_ops.cpp", "permute.hip", "mx_convert.hip", "mx_matmul.hip",
+           "fp8_ops.cpp", "route_scores.hip", "fp8_convert.hip", "fp8_matmul.hip", "activate.hip"]
 
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
          # packed fp32 VALU ops stay off: plain scalar fp32 everywhere

@@ -9,6 +9,7 @@
 // scale byte; the lane half h is the block of the two that the step contracts.
 // The result: register i of lane l is row 8 (i/4) + 4 h + i%4, column c.
 #include "expert_ops.h"
+#include "expert_tiles.h"
 #include "mx_shape.h"
 #include "qmoe_internal.h"
 #include "rowio.h"
@@ -18,7 +19,6 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr int kMaxExperts = 1024;
 constexpr int kE2M1 = 4;  // operand format code of the scaled matrix instructions
 
 __device__ inline i32x8 operand(u32x4 v)
@@ -99,17 +99,6 @@ __device__ inline int lane_now()
 __device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, void* to)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, lane_offset, 0, 0, 0);
-}
-
-template <int DT>
-__device__ inline uint32_t pack_pair(float lo, float hi)
-{
-    if constexpr (DT == kBF16) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
-    } else {
-        return pack2(Dt<kF16>::from_float(lo), Dt<kF16>::from_float(hi));
-    }
 }
 
 // Stores one block of 32 x 32 results: lane (c, half) holds row c, columns
@@ -220,86 +209,6 @@ __device__ inline u32x4 load_scale_chunk(const uint8_t* p, int chunk, int left)
         hi = left & 8 ? rest : 0;
     }
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-}
-
-// m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
-// Offsets are clamped to [0, rows] and mx_items() bounds the count, so no table
-// content leads outside the output.  scratch: E + 1 words of LDS.
-template <int BM, int THREADS>
-__device__ void build_tile_list(int* first, int* scratch, const int32_t* offsets, int E, int rows)
-{
-    for (int e = threadIdx.x; e <= E; e += THREADS) {
-        scratch[e] = offsets ? min(max(offsets[e], 0), rows) : e * rows;
-    }
-    __syncthreads();
-    if (threadIdx.x < kWave) {
-        const int lane = threadIdx.x, per = (E + kWave - 1) / kWave;  // consecutive experts a lane
-        auto tiles = [&](int e) { return e < E ? (max(scratch[e + 1] - scratch[e], 0) + BM - 1) / BM : 0; };
-        int sum = 0;
-        for (int i = 0; i < per; ++i) sum += tiles(lane * per + i);
-        int incl = sum;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int y = __shfl_up(incl, d, kWave);
-            if (lane >= d) incl += y;
-        }
-        int run = incl - sum;
-        for (int i = 0; i < per; ++i) {
-            const int e = lane * per + i;
-            if (e < E) first[e] = run;
-            run += tiles(e);
-        }
-        if (lane == kWave - 1) first[E] = run;
-    }
-    __syncthreads();
-}
-
-// Reads through it are scalar and wait for no vector memory; what it points to does not change
-// while the kernel runs.
-__device__ inline const __attribute__((address_space(4))) int32_t* constant(const int32_t* p)
-{
-    return (const __attribute__((address_space(4))) int32_t*)p;
-}
-
-// The workgroups that run on a die at a time (32 of the largest tile) share rows and weights in its
-// L2: bands of 8 m-tiles make that about 8 row blocks and 4 weight blocks, in place of one column of
-// 32 (8192^3: 281 -> 246 us; bands of 4 and of 12 were slower).
-constexpr int kBand = 8;
-
-struct TileItem {
-    int expert;
-    int row0;
-    int n;   // rows; 0: no item
-    int n0;  // first column
-};
-
-// offset(e) gives expert e's clamped offset.
-template <int BM, int BN, class Offset>
-__device__ TileItem item_at(const int* first, Offset offset, int E, int n_tiles, int item, int end)
-{
-    if (item >= end) return TileItem{0, 0, 0, 0};
-    int lo = 0, hi = E - 1;  // the last expert whose first item is <= item
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] * n_tiles <= item) lo = mid; else hi = mid - 1;
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const int base = __builtin_amdgcn_readfirstlane(first[lo]);
-    const int m_tiles = __builtin_amdgcn_readfirstlane(first[lo + 1]) - base;
-    // bands of up to kBand m-tiles, in a band neighbouring items share the weights
-    int local = item - base * n_tiles;
-    int m0 = 0, band = m_tiles;
-    if (m_tiles > kBand) {
-        const int bands = (m_tiles + kBand - 1) / kBand;
-        band = (m_tiles + bands - 1) / bands;
-        m0 = local / (band * n_tiles) * band;
-        local -= m0 * n_tiles;
-        band = min(band, m_tiles - m0);
-    }
-    const int nt = local / band;
-    const int r_lo = offset(lo), r_hi = offset(lo + 1);
-    const int row0 = r_lo + (m0 + local - nt * band) * BM;
-    return TileItem{lo, row0, min(BM, r_hi - row0), nt * BN};
 }
 
 template <int DT, int MT, int NT, int WM, int WN, int STAGES, bool WHOLE>
