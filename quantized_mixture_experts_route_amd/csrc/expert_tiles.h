@@ -22,6 +22,40 @@ __device__ inline uint32_t pack_pair(float lo, float hi)
     }
 }
 
+// Stores 16 rows of 32 columns of 16-bit values: lane l's v holds the eight columns from
+// 8 (l / 32) + 16 (l / 16 % 2) on of row l % 16.  `out` is the first row and column; rows and cols say how
+// many of them exist (WHOLE: all).
+template <bool WHOLE>
+__device__ inline void store_sixteen(uint16_t* out, int N, int rows, int cols, u32x4 v, int lane)
+{
+    const int row = lane & 15, col = 8 * (lane >> 5) + 16 * ((lane >> 4) & 1);
+    uint16_t* p = out + (int64_t)row * N + col;
+    if (WHOLE && (((uintptr_t)out | (uintptr_t)N << 1) & 2)) {
+        // rows that start between two words: they are stored one column on, in whole words, with
+        // the first column of the neighbour's eight at the end; columns 0 and 31 on their own
+        // (MXFP4, 18498 rows of 2175 columns: 90 us, with 16-byte stores that split words 105)
+        const uint32_t next = (uint32_t)__shfl((int)v[0], lane < 32 ? lane + 32 : lane - 16, kWave);
+        const bool odd = (uintptr_t)p & 2;
+        if (odd) {
+            if (col == 0) p[0] = (uint16_t)v[0];
+            if (col == 24) p[7] = (uint16_t)(v[3] >> 16);
+            v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16 | next << 16};
+        }
+        __builtin_memcpy(p + odd, &v, 12);
+        if (!odd || col < 24) __builtin_memcpy(p + odd + 6, (const char*)&v + 12, 4);
+        return;
+    }
+    if (!WHOLE && row >= rows) return;
+    if (WHOLE || col + 8 <= cols) {
+        __builtin_memcpy(p, &v, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (col + i < cols) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
 // m-tiles of each expert in LDS: first[e] .. first[e + 1] of the tile list.
 // Offsets are clamped to [0, rows] and mx_items() bounds the count, so no table
 // content leads outside the output.  scratch: E + 1 words of LDS.

@@ -16,6 +16,7 @@
 // need the operands as f16 at half the rate, and are refused.
 #include "expert_tiles.h"
 #include "fp8_ops.h"
+#include "mx_shape.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {
@@ -29,82 +30,360 @@ __device__ inline i32x8 operand(u32x4 a, u32x4 b)
     return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
+// f(0), ..., each with its number as a constant.
+template <int FROM, int TO, class F>
+__device__ inline void static_for(F f)
+{
+    if constexpr (FROM < TO) {
+        f(std::integral_constant<int, FROM>{});
+        static_for<FROM + 1, TO>(f);
+    }
+}
+
 // A block's product on its own: the scales are applied to it in float32.
 __device__ inline f32x4 block_product(i32x8 w, i32x8 x)
 {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{}, kE4M3, kE4M3, 0, 0, 0, 0);
 }
 
-constexpr int kThreads = 256;
+// A workgroup of WM x WN wavefronts computes BM = 16 MT WM rows against BN = 16 NT WN weight rows; a
+// wavefront MT x NT blocks of 16 x 16.  W is the instruction's first operand, so a lane's registers run
+// along n, and the row scale is the lane's own while the weight scale is the wavefront's: one factor for
+// each 16 rows and block of 128, and one multiply-add for each result and block.
+//
+// K runs in steps of one block of 128: 128 bytes of codes a row, a whole cache line, written to LDS by the
+// load itself (buffer_load ... lds) into one of STAGES stages, with the rows' scales of the block.  The one
+// barrier of a step stands before its last group of products: then every operand of the step is in registers,
+// its stage takes the loads of the step STAGES ahead, and the next step has landed.  Loads run on over the end
+// of a tile into the workgroup's next one, so only its first tile waits for memory.
+//
+// LDS rows are 128 bytes (32 banks); the 16-byte chunk of row r sits in slot chunk ^ (r / 2 % 8), so that 16
+// rows read at one chunk cover all 64 banks.
+//
+// WHOLE: K is a multiple of 128 with a step for each stage.  Otherwise codes and scales behind the row's end
+// are read out of the buffer's bounds, which gives 0.
+constexpr int kStepBytes = kFp8Block;  // codes of one row and step
+constexpr int kSlots = kWave;          // scales a wavefront loads in a step
 
-// A wavefront computes 16 rows against 16 weight rows, operands straight from memory.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void simple_kernel(Fp8MatmulArgs a)
+// Bytes that a tile reads of codes or scales; its descriptor from byte `at` on.
+struct Span {
+    const uint8_t* base;
+    uint32_t bytes;
+    __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
+    {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0, mx_bytes_left(bytes, at), 0x00020000);
+    }
+};
+
+// BYTES a lane from the buffer to LDS at `to` + BYTES * lane (to is uniform); zeros where the lane's offset is
+// not in the buffer.
+template <int BYTES>
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, void* to)
 {
-    typedef typename RowType<DT>::Raw Raw;
-    constexpr int BM = 16, BN = 64;
-    __shared__ int first[kMaxExperts + 1], scratch[kMaxExperts + 1];
-    build_tile_list<BM, kThreads>(first, scratch, a.offsets, a.E, a.rows);
+    auto* const lds = (__attribute__((address_space(3))) void*)to;
+    if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 16, lane_offset, 0, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 4, lane_offset, 0, 0, 0);
+}
+
+// Stores two neighbouring blocks of 16 x 16 results: lane 16 g + c holds row c, columns 4 g + i of either in
+// register i.  `out` is the first row and column; rows and cols say how many of them exist (WHOLE: all).
+template <int DT, bool WHOLE>
+__device__ inline void store_blocks(uint16_t* out, int N, int rows, int cols, const f32x4& left, const f32x4& right, int lane)
+{
+    // lane groups trade columns, so that each lane holds eight neighbours (store_sixteen's order)
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto t = __builtin_amdgcn_permlane16_swap(pack_pair<DT>(left[2 * i], left[2 * i + 1]),
+                                                        pack_pair<DT>(right[2 * i], right[2 * i + 1]), false, false);
+        v[i] = t[0];
+        v[2 + i] = t[1];
+    }
+    store_sixteen<WHOLE>(out, N, rows, cols, v, lane);
+}
+
+template <int DT, int MT, int NT, int WM, int WN, int STAGES, bool WHOLE>
+__global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
+{
+    constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, ROWS = BM + BN;
+    constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    constexpr int LOADS_A = BM / 8 / WAVES, LOADS_W = BN / 8 / WAVES;  // code loads of a wavefront and step: 8 rows each
+    constexpr int LOADS = LOADS_A + LOADS_W + 1;                       // and one of scales
+    constexpr int A_SLOTS = (BM + kSlots - 1) / kSlots;                // wavefronts that load rows' scales; the next the weights'
+    constexpr int N_BLOCKS = (BN + kFp8Block - 1) / kFp8Block;
+    static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && WAVES % 2 == 0, "load split");
+    static_assert(A_SLOTS < WAVES && NT % 2 == 0 && NT * 16 <= kFp8Block, "a wavefront's columns share their scale");
+
+    // one array for all of it: between arrays of their own the compiler tells apart what a load to
+    // LDS writes and waits for every such load before it reads LDS
+    constexpr int SCALES = ROWS * kStepBytes, STAGE = SCALES + WAVES * kSlots * 4;
+    constexpr int LIST = STAGES * STAGE, SOURCE = LIST + (kMaxExperts + 1) * 4;
+    static_assert(STAGE >= (kMaxExperts + 1) * 4, "the offsets' place");
+    __shared__ __align__(16) uint8_t lds[SOURCE + 2 * BM * 4];
+    int* const first = reinterpret_cast<int*>(lds + LIST);
+    int* const source = reinterpret_cast<int*>(lds + SOURCE);
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int K = a.K, blocks = (K + kFp8Block - 1) / kFp8Block, n_blocks = (a.N + kFp8Block - 1) / kFp8Block;
+    const int steps = max(blocks, STAGES);  // the loading side is STAGES ahead and stays within one tile
+
+    // the last stage's space, not loaded before the first barrier, holds the offsets for the first item
+    int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
+    build_tile_list<BM, THREADS>(first, scratch, a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
     const int total = mx_items(first[a.E], n_tiles, a.rows, BM, a.E);
-    if (a.offsets) {  // rows behind the last expert's are zero
-        const int64_t lo = (int64_t)scratch[a.E] * a.N, hi = (int64_t)a.rows * a.N;
-        for (int64_t i = lo + blockIdx.x * (int64_t)kThreads + threadIdx.x; i < hi; i += (int64_t)gridDim.x * kThreads) {
-            ((Raw*)a.out)[i] = 0;
+    // workgroups go to the 8 dies in turn: each die takes one run of items, so
+    // that the workgroups of a die share rows and weights in its L2
+    const int per_die = gridDim.x / 8;
+    const int die = blockIdx.x % 8;
+    const int end = (int)((int64_t)total * (die + 1) / 8);
+    int next_item = (int)((int64_t)total * die / 8) + blockIdx.x / 8;
+
+    // rows behind the last expert's are zero
+    if (a.offsets) {
+        const int64_t lo = (int64_t)min(max(a.offsets[a.E], 0), a.rows) * a.N, hi = (int64_t)a.rows * a.N;
+        for (int64_t i = lo + (blockIdx.x * (int64_t)THREADS + threadIdx.x) * 8; i < hi; i += (int64_t)gridDim.x * THREADS * 8) {
+            if (i + 8 <= hi) {
+                store_vec<uint16_t, 8>((uint16_t*)a.out + i, RowVec<uint16_t, 8>{});
+            } else {
+                for (int64_t q = i; q < hi; ++q) ((uint16_t*)a.out)[q] = 0;
+            }
         }
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-    const int blocks = (a.K + kFp8Block - 1) / kFp8Block, n_blocks = (a.N + kFp8Block - 1) / kFp8Block;
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const TileItem t = item_at<BM, BN>(first, [&](int e) { return scratch[e]; }, a.E, n_tiles, item, total);
-        const int n0 = t.n0 + wave * 16;
-        if (n0 >= a.N) continue;
-        const int r = t.row0 + min(c, t.n - 1);
-        int64_t source = r;
-        bool there = true;
-        if (a.sorted_routes) {
-            const int route = a.sorted_routes[r];
-            there = route >= 0 && route / a.top_k < a.a_rows;
-            source = there ? route / a.top_k : 0;
+
+    // ---- the loading side: an item and a step, up to STAGES steps ahead
+    TileItem load_tile;
+    int load_step = 0;
+    const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+    uint32_t code_at[LOADS_A];  // byte offset of the lane's chunk at step 0
+    const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K + load_chunk;  // rows behind N: out of bounds
+    uint32_t scale_at;          // byte offset of the lane's scale at step 0
+    Span a_span, w_span, scale_span;
+    // The next item, found between two tiles, where registers are free; and in LDS its rows' source rows in a
+    // (from the tile's first row where there are no routes; -1: outside; rows behind the tile's repeat its last).
+    TileItem next_tile;
+    int found = 0;  // tables of source rows take turns
+    auto find_tile = [&](auto offset) {
+        next_tile = item_at<BM, BN>(first, offset, a.E, n_tiles, next_item, end);
+        next_item += per_die;
+        found ^= BM;
+        for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
+            int row = min(r, next_tile.n - 1);
+            if (a.sorted_routes) {
+                const int route = a.sorted_routes[next_tile.row0 + row];
+                row = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
+            }
+            source[found + r] = row;
         }
-        const uint8_t* x = a.a_codes + source * a.K;
-        const uint8_t* w = a.w_codes + ((int64_t)t.expert * a.N + min(n0 + c, a.N - 1)) * a.K;
-        const float* sa = a.a_scales + source * blocks;
-        const float* sw = a.w_scales + ((int64_t)t.expert * n_blocks + n0 / kFp8Block) * blocks;
-        f32x4 acc = {};
-        for (int b = 0; b < blocks; ++b) {
-            u32x4 vx[2] = {}, vw[2] = {};
+    };
+    auto offset_of = [&](int e) { return a.offsets ? min(max(constant(a.offsets)[e], 0), a.rows) : e * a.rows; };
+    auto start_tile = [&]() {  // all but what goes by the source rows
+        load_tile = next_tile;
+        load_step = 0;
+        const TileItem& t = load_tile;
+        const bool on = t.n > 0;
+        const int w_rows = on ? min(BN, a.N - t.n0) : 0;
+        const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
+        w_span = Span{a.w_codes + w0 * K, (uint32_t)(w_rows * K)};
+        const int64_t a0 = a.sorted_routes ? 0 : t.row0;
+        const int64_t a_rows = !on ? 0 : a.sorted_routes ? a.a_rows : t.n;
+        a_span = Span{a.a_codes + a0 * K, (uint32_t)(a_rows * K)};
+        if (wave < A_SLOTS) {
+            scale_span = Span{(const uint8_t*)(a.a_scales + a0 * blocks), (uint32_t)(a_rows * blocks * 4)};
+        } else {
+            const int64_t s0 = on ? (int64_t)t.expert * n_blocks + t.n0 / kFp8Block : 0;
+            const int rows = on && wave == A_SLOTS ? min(N_BLOCKS, n_blocks - t.n0 / kFp8Block) : 0;
+            scale_span = Span{(const uint8_t*)(a.w_scales + s0 * blocks), (uint32_t)(rows * blocks * 4)};
+            scale_at = lane < rows ? lane * (uint32_t)blocks * 4 : kMxOutside;
+        }
+    };
+    auto start_rows = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = b * kFp8Block + g * 32 + h * 16;
-                if (k < a.K) {
-                    if (there) vx[h] = *reinterpret_cast<const u32x4*>(x + k);
-                    vw[h] = *reinterpret_cast<const u32x4*>(w + k);
+        for (int j = 0; j < LOADS_A; ++j) {
+            const int row = source[found + (j * WAVES + wave) * 8 + (lane >> 3)];
+            code_at[j] = row < 0 ? kMxOutside : row * (uint32_t)K + load_chunk;
+        }
+        if (wave < A_SLOTS) {
+            const int row = source[found + min(wave * kSlots + lane, BM - 1)];
+            scale_at = row < 0 ? kMxOutside : row * (uint32_t)blocks * 4;
+        }
+    };
+    auto load_weights = [&](int stage) {
+        const uint32_t at = (uint32_t)load_step * kStepBytes;
+        const __amdgpu_buffer_rsrc_t buf = w_span.from(at);
+        const bool in = WHOLE || at + load_chunk < (uint32_t)K;
+#pragma unroll
+        for (int j = 0; j < LOADS_W; ++j) {
+            load_to_lds<16>(buf, in ? w_at + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
+                            lds + stage * STAGE + (BM + (j * WAVES + wave) * 8) * kStepBytes);
+        }
+    };
+    auto load_rows = [&](int stage) {  // and all scales
+        const uint32_t at = (uint32_t)load_step * kStepBytes;
+        const __amdgpu_buffer_rsrc_t buf = a_span.from(at);
+        const bool in = WHOLE || at + load_chunk < (uint32_t)K;
+#pragma unroll
+        for (int j = 0; j < LOADS_A; ++j) {
+            load_to_lds<16>(buf, in ? code_at[j] : kMxOutside, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
+        }
+        load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside,
+                       lds + stage * STAGE + SCALES + wave * kSlots * 4);
+        ++load_step;
+    };
+    find_tile([&](int e) { return scratch[e]; });
+    start_tile();
+    load_weights(0);  // weights do not wait for the table of rows
+    __syncthreads();
+    start_rows();
+    load_rows(0);
+#pragma unroll
+    for (int i = 1; i < STAGES - 1; ++i) {
+        load_weights(i);
+        load_rows(i);
+    }
+    find_tile(offset_of);
+
+    // ---- the computing side: chunks g and g + 4 of row c are lane 16 g + c's
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t read_lo = c * (uint32_t)kStepBytes + (uint32_t)(g ^ (c >> 1)) * 16, read_hi = read_lo ^ 64;
+    i32x8 x[MT], w[2];
+    float sa[MT], sw;
+    const uint32_t x_base = wm * MT * 16 * kStepBytes, w_base = (BM + wn * NT * 16) * kStepBytes;
+    auto read_operand = [&](uint32_t at) {
+        return operand(*reinterpret_cast<const u32x4*>(lds + at + read_lo), *reinterpret_cast<const u32x4*>(lds + at + read_hi));
+    };
+    auto read_scales = [&](int stage) {
+        const uint8_t* from = lds + stage * STAGE + SCALES;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sa[j] = *reinterpret_cast<const float*>(from + ((wm * MT + j) * 16 + c) * 4);
+        sw = *reinterpret_cast<const float*>(from + (A_SLOTS * kSlots + wn * NT * 16 / kFp8Block) * 4);
+    };
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
+    load_weights(STAGES - 1);
+    load_rows(STAGES - 1);
+    read_scales(0);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) x[j] = read_operand(x_base + j * 16 * kStepBytes);
+    w[0] = read_operand(w_base);
+    int stage = 0;
+    while (load_tile.n > 0) {
+        const TileItem tile = load_tile;
+        // wavefronts whose rows lie behind the tile's leave their products out
+        const bool active = wm * MT * 16 < tile.n;
+        f32x4 acc[NT][MT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{};
+        }
+        for (int s = 0; s < steps; ++s) {
+            const int next = stage + 1 == STAGES ? 0 : stage + 1;
+            float f[MT];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) f[j] = sa[j] * sw;
+            // product t's multiply-adds run behind product t + LAG
+            constexpr int LAG = 2, COUNT = NT * MT;
+            f32x4 p[LAG + 1];
+            auto add = [&](auto t) {
+                constexpr int i = decltype(t)::value / MT, j = decltype(t)::value % MT;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(f[j], p[decltype(t)::value % (LAG + 1)][q], acc[i][j][q]);
+                asm volatile("" : "+v"(acc[i][j]));
+            };
+            auto product = [&](auto t) {
+                constexpr int n = decltype(t)::value, i = n / MT, j = n % MT;
+                p[n % (LAG + 1)] = block_product(w[i & 1], x[j]);
+                asm volatile("" : "+v"(p[n % (LAG + 1)]));  // in this place
+                if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
+            };
+            auto read_row = [&](auto j) { x[j] = read_operand(next * STAGE + x_base + j * 16 * kStepBytes); };
+            static_for<0, NT>([&](auto row) {
+                constexpr int i = decltype(row)::value;
+                if constexpr (i + 1 < NT) {
+                    w[(i + 1) & 1] = read_operand(stage * STAGE + w_base + (i + 1) * 16 * kStepBytes);
+                } else {
+                    // the next step has landed once no more than the loads behind it are left
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS) : "memory");
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    read_scales(next);
+                    w[0] = read_operand(next * STAGE + w_base);
+                    if (load_step == steps) {
+                        start_tile();
+                        start_rows();
+                    }
+                    load_weights(stage);
+                    load_rows(stage);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                if (active) {
+                    static_for<0, MT>([&](auto column) {
+                        constexpr int j = decltype(column)::value;
+                        product(std::integral_constant<int, i * MT + j>{});
+                        if constexpr (i + 1 == NT) read_row(column);
+                    });
+                } else if constexpr (i + 1 == NT) {
+                    static_for<0, MT>(read_row);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if (active) {
+                static_for<COUNT - LAG, COUNT>([&](auto t) { add(t); });
             }
-            const f32x4 p = block_product(operand(vw[0], vw[1]), operand(vx[0], vx[1]));
-            const float f = there ? sa[b] * sw[b] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, p[i], acc[i]);
+            stage = next;
         }
-        if (c < t.n) {
+        find_tile(offset_of);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = n0 + 4 * g + i;
-                if (n < a.N) ((Raw*)a.out)[(int64_t)(t.row0 + c) * a.N + n] = RowType<DT>::round(acc[i]);
+        for (int j = 0; j < MT; ++j) {
+            const int m0 = (wm * MT + j) * 16;
+#pragma unroll
+            for (int i = 0; i < NT; i += 2) {
+                const int n = tile.n0 + (wn * NT + i) * 16;
+                uint16_t* out = (uint16_t*)a.out + (int64_t)(tile.row0 + m0) * a.N + n;
+                if (tile.n - m0 >= 16 && a.N - n >= 32) store_blocks<DT, true>(out, a.N, 16, 32, acc[i][j], acc[i + 1][j], lane);
+                else store_blocks<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j], acc[i + 1][j], lane);
             }
         }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS behind the workgroup's end
+}
+
+// wgs_per_cu: as many as fit by LDS and registers.
+template <int DT, int MT, int NT, int WM, int WN, int STAGES>
+hipError_t launch_tiled(const Fp8MatmulArgs& a, int wgs_per_cu, hipStream_t s)
+{
+    constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN;
+    // at most one partial tile for every expert with rows
+    const int64_t experts = a.E < a.rows ? a.E : a.rows;
+    const int64_t items = (experts + (a.rows - experts) / BM) * ((a.N + BN - 1) / BN);
+    int64_t grid = (items + 7) / 8 * 8;
+    if (grid > kMxCUs * wgs_per_cu) grid = kMxCUs * wgs_per_cu;
+    const dim3 threads(64 * WM * WN);
+    if (a.K % kFp8Block == 0 && a.K / kFp8Block >= STAGES) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), threads, s, a);
+    else launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), threads, s, a);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_by_shape(const Fp8MatmulArgs& a, hipStream_t s)
+{
+    switch (mx_tile(a.E, a.N, a.K, a.rows)) {
+    case MxTile::k32x64s4: return launch_tiled<DT, 2, 2, 1, 2, 4>(a, 2, s);
+    case MxTile::k64x128s4: return launch_tiled<DT, 2, 4, 2, 2, 4>(a, 1, s);
+    case MxTile::k128x128s4: return launch_tiled<DT, 4, 4, 2, 2, 4>(a, 1, s);
+    case MxTile::k64x128s2: return launch_tiled<DT, 2, 4, 2, 2, 2>(a, 2, s);
+    case MxTile::k128x128s2: return launch_tiled<DT, 4, 4, 2, 2, 2>(a, 2, s);
+    case MxTile::k256x256s2: break;
+    }
+    return launch_tiled<DT, 4, 8, 4, 2, 2>(a, 1, s);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& a, hipStream_t s)
 {
-    const dim3 grid(8 * kMxCUs);
-    if (a.dtype == kBF16) launch(simple_kernel<kBF16>, grid, dim3(kThreads), s, a);
-    else launch(simple_kernel<kF16>, grid, dim3(kThreads), s, a);
-    return hipGetLastError();
+    return a.dtype == kBF16 ? launch_by_shape<kBF16>(a, s) : launch_by_shape<kF16>(a, s);
 }
 
 }  // namespace qmoe

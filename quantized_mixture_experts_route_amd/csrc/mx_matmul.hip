@@ -110,21 +110,21 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
     typedef typename RowType<DT>::Raw Raw;
     constexpr int V = 16 / sizeof(Raw);
     const int c = lane & 31, half = lane >> 5;
-    auto store = [&](int row, int col, const u32x4& v) {
-        if (!WHOLE && row >= rows) return;
-        RowVec<Raw, V> y;
-        __builtin_memcpy(&y, &v, 16);
-        Raw* p = out + (int64_t)row * N + col;
-        if (WHOLE || col + V <= cols) {
-            store_vec<Raw, V>(p, y);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (col + i < cols) p[i] = y.v[i];
-            }
-        }
-    };
     if constexpr (DT == kF32) {
+        auto store = [&](int row, int col, const u32x4& v) {
+            if (!WHOLE && row >= rows) return;
+            RowVec<Raw, V> y;
+            __builtin_memcpy(&y, &v, 16);
+            Raw* p = out + (int64_t)row * N + col;
+            if (WHOLE || col + V <= cols) {
+                store_vec<Raw, V>(p, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (col + i < cols) p[i] = y.v[i];
+                }
+            }
+        };
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             u32x4 v;
@@ -154,30 +154,8 @@ __device__ inline void store_block(typename RowType<DT>::Raw* out, int N, int ro
             v[0][i] = t[0];
             v[1][i] = t[1];
         }
-        const int col = 8 * half + 16 * ((lane >> 4) & 1);
-        if (WHOLE && (((uintptr_t)out | (uintptr_t)N << 1) & 2)) {
-            // rows that start between two words: they are stored one column on, in whole words, with
-            // the first column of the neighbour's eight at the end; columns 0 and 31 on their own
-            // (18498 rows of 2175 columns: 90 us, with 16-byte stores that split words 105)
-            const int neighbour = lane < 32 ? lane + 32 : lane - 16;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                Raw* p = out + (int64_t)(16 * q + (lane & 15)) * N + col;
-                const uint32_t next = (uint32_t)__shfl((int)v[q][0], neighbour, kWave);
-                const bool odd = (uintptr_t)p & 2;
-                if (odd) {
-                    if (col == 0) p[0] = (Raw)v[q][0];
-                    if (col == 24) p[7] = (Raw)(v[q][3] >> 16);
-                    v[q] = u32x4{v[q][0] >> 16 | v[q][1] << 16, v[q][1] >> 16 | v[q][2] << 16,
-                                 v[q][2] >> 16 | v[q][3] << 16, v[q][3] >> 16 | next << 16};
-                }
-                __builtin_memcpy(p + odd, &v[q], 12);
-                if (!odd || col < 24) __builtin_memcpy(p + odd + 6, (const char*)&v[q] + 12, 4);
-            }
-            return;
-        }
-        store(lane & 15, col, v[0]);
-        store(16 + (lane & 15), col, v[1]);
+        store_sixteen<WHOLE>(out, N, rows, cols, v[0], lane);
+        store_sixteen<WHOLE>(out + (int64_t)16 * N, N, rows - 16, cols, v[1], lane);
     }
 }
 
