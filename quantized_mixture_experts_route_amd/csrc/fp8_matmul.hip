@@ -69,11 +69,26 @@ constexpr int kSlots = kWave;          // scales a wavefront loads in a step
 struct Span {
     const uint8_t* base;
     uint32_t bytes;
+    // Uniform, which the compiler does not see of what came out of LDS or through a multiplication on the
+    // vector units: without readfirstlane each load runs in a loop over its lanes' descriptors (8192 x 28672
+    // x 4096 over 8 experts: 1073 -> TODO us).
     __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
     {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0, mx_bytes_left(bytes, at), 0x00020000);
+        const uint64_t p = (uint64_t)(base + at);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+        return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
+                                                 __builtin_amdgcn_readfirstlane(mx_bytes_left(bytes, at)), 0x00020000);
     }
 };
+
+// The lane, worked out where it stands.  What is made from it needs no register over the K loop; what the
+// compiler keeps there is spilled, and a reload waits for every load and store before it.
+__device__ inline int lane_now()
+{
+    int zero = 0;
+    asm volatile("" : "+s"(zero));
+    return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+}
 
 // BYTES a lane from the buffer to LDS at `to` + BYTES * lane (to is uniform); zeros where the lane's offset is
 // not in the buffer.
@@ -109,6 +124,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
     constexpr int LOADS_A = BM / 8 / WAVES, LOADS_W = BN / 8 / WAVES;  // code loads of a wavefront and step: 8 rows each
     constexpr int LOADS = LOADS_A + LOADS_W + 1;                       // and one of scales
+    constexpr int FIRST = LOADS_A + LOADS_W / 2 + 1;                   // those that the first half of a step issues
     constexpr int A_SLOTS = (BM + kSlots - 1) / kSlots;                // wavefronts that load rows' scales; the next the weights'
     constexpr int N_BLOCKS = (BN + kFp8Block - 1) / kFp8Block;
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && WAVES % 2 == 0, "load split");
@@ -123,7 +139,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     int* const first = reinterpret_cast<int*>(lds + LIST);
     int* const source = reinterpret_cast<int*>(lds + SOURCE);
 
-    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int K = a.K, blocks = (K + kFp8Block - 1) / kFp8Block, n_blocks = (a.N + kFp8Block - 1) / kFp8Block;
@@ -133,7 +148,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     int* const scratch = reinterpret_cast<int*>(lds + (STAGES - 1) * STAGE);
     build_tile_list<BM, THREADS>(first, scratch, a.offsets, a.E, a.rows);
     const int n_tiles = (a.N + BN - 1) / BN;
-    const int total = mx_items(first[a.E], n_tiles, a.rows, BM, a.E);
+    const int total = __builtin_amdgcn_readfirstlane(mx_items(first[a.E], n_tiles, a.rows, BM, a.E));
     // workgroups go to the 8 dies in turn: each die takes one run of items, so
     // that the workgroups of a die share rows and weights in its L2
     const int per_die = gridDim.x / 8;
@@ -156,9 +171,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     // ---- the loading side: an item and a step, up to STAGES steps ahead
     TileItem load_tile;
     int load_step = 0;
-    const uint32_t load_chunk = (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16;
+    auto load_chunk = [&](int lane) { return (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16; };
     uint32_t code_at[LOADS_A];  // byte offset of the lane's chunk at step 0
-    const uint32_t w_at = (wave * 8 + (lane >> 3)) * (uint32_t)K + load_chunk;  // rows behind N: out of bounds
+    auto w_at = [&](int lane) { return (wave * 8 + (lane >> 3)) * (uint32_t)K + load_chunk(lane); };  // rows behind N: out of bounds
     uint32_t scale_at;          // byte offset of the lane's scale at step 0
     Span a_span, w_span, scale_span;
     // The next item, found between two tiles, where registers are free; and in LDS its rows' source rows in a
@@ -169,7 +184,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
         next_tile = item_at<BM, BN>(first, offset, a.E, n_tiles, next_item, end);
         next_item += per_die;
         found ^= BM;
-        for (int r = threadIdx.x; r < BM && next_tile.n > 0; r += THREADS) {
+        for (int r = wave * kWave + lane_now(); r < BM && next_tile.n > 0; r += THREADS) {
             int row = min(r, next_tile.n - 1);
             if (a.sorted_routes) {
                 const int route = a.sorted_routes[next_tile.row0 + row];
@@ -196,77 +211,96 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
             const int64_t s0 = on ? (int64_t)t.expert * n_blocks + t.n0 / kFp8Block : 0;
             const int rows = on && wave == A_SLOTS ? min(N_BLOCKS, n_blocks - t.n0 / kFp8Block) : 0;
             scale_span = Span{(const uint8_t*)(a.w_scales + s0 * blocks), (uint32_t)(rows * blocks * 4)};
+            const int lane = lane_now();
             scale_at = lane < rows ? lane * (uint32_t)blocks * 4 : kMxOutside;
         }
     };
     auto start_rows = [&]() {
+        const int lane = lane_now();
 #pragma unroll
         for (int j = 0; j < LOADS_A; ++j) {
             const int row = source[found + (j * WAVES + wave) * 8 + (lane >> 3)];
-            code_at[j] = row < 0 ? kMxOutside : row * (uint32_t)K + load_chunk;
+            code_at[j] = row < 0 ? kMxOutside : row * (uint32_t)K + load_chunk(lane);
         }
         if (wave < A_SLOTS) {
-            const int row = source[found + min(wave * kSlots + lane, BM - 1)];
+            // a lane's MT rows' scales lie side by side
+            const int at = wave * kSlots + lane, block = at / (16 * MT), in = at % (16 * MT);
+            const int row = source[found + min(block * 16 * MT + in % MT * 16 + in / MT, BM - 1)];
             scale_at = row < 0 ? kMxOutside : row * (uint32_t)blocks * 4;
         }
     };
-    auto load_weights = [&](int stage) {
+    // The weights' halves: rows that a wavefront's first and last NT / 2 blocks read, 8 WAVES rows in turn.
+    static_assert(NT * 8 == 8 * WAVES, "a load of all wavefronts covers half of one's columns");
+    auto load_weights = [&](int stage, int half) {
         const uint32_t at = (uint32_t)load_step * kStepBytes;
         const __amdgpu_buffer_rsrc_t buf = w_span.from(at);
-        const bool in = WHOLE || at + load_chunk < (uint32_t)K;
+        const uint32_t row = w_at(lane_now());
+        const bool in = WHOLE || at + load_chunk(lane_now()) < (uint32_t)K;
 #pragma unroll
-        for (int j = 0; j < LOADS_W; ++j) {
-            load_to_lds<16>(buf, in ? w_at + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
+        for (int j = half; j < LOADS_W; j += 2) {
+            load_to_lds<16>(buf, in ? row + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
                             lds + stage * STAGE + (BM + (j * WAVES + wave) * 8) * kStepBytes);
         }
     };
     auto load_rows = [&](int stage) {  // and all scales
         const uint32_t at = (uint32_t)load_step * kStepBytes;
         const __amdgpu_buffer_rsrc_t buf = a_span.from(at);
-        const bool in = WHOLE || at + load_chunk < (uint32_t)K;
+        const bool in = WHOLE || at + load_chunk(lane_now()) < (uint32_t)K;
 #pragma unroll
         for (int j = 0; j < LOADS_A; ++j) {
             load_to_lds<16>(buf, in ? code_at[j] : kMxOutside, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
         }
         load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside,
                        lds + stage * STAGE + SCALES + wave * kSlots * 4);
+    };
+    auto load_first = [&](int stage) {
+        load_rows(stage);
+        load_weights(stage, 0);
+    };
+    auto load_second = [&](int stage) {
+        load_weights(stage, 1);
         ++load_step;
     };
-    find_tile([&](int e) { return scratch[e]; });
+    find_tile([&](int e) { return __builtin_amdgcn_readfirstlane(scratch[e]); });
     start_tile();
-    load_weights(0);  // weights do not wait for the table of rows
+    load_weights(0, 0);  // weights do not wait for the table of rows
+    load_weights(0, 1);
     __syncthreads();
     start_rows();
     load_rows(0);
+    ++load_step;
 #pragma unroll
     for (int i = 1; i < STAGES - 1; ++i) {
-        load_weights(i);
-        load_rows(i);
+        load_first(i);
+        load_second(i);
     }
     find_tile(offset_of);
 
     // ---- the computing side: chunks g and g + 4 of row c are lane 16 g + c's
-    const int c = lane & 15, g = lane >> 4;
+    const int c = lane_now() & 15, g = lane_now() >> 4;
     const uint32_t read_lo = c * (uint32_t)kStepBytes + (uint32_t)(g ^ (c >> 1)) * 16, read_hi = read_lo ^ 64;
-    i32x8 x[MT], w[2];
-    float sa[MT], sw;
+    constexpr int W_BUFFERS = NT < 4 ? NT : 4;  // two blocks ahead
+    i32x8 x[MT], w[W_BUFFERS];
+    typedef float RowScales __attribute__((ext_vector_type(MT)));
+    RowScales sa;
+    float sw;
     const uint32_t x_base = wm * MT * 16 * kStepBytes, w_base = (BM + wn * NT * 16) * kStepBytes;
     auto read_operand = [&](uint32_t at) {
         return operand(*reinterpret_cast<const u32x4*>(lds + at + read_lo), *reinterpret_cast<const u32x4*>(lds + at + read_hi));
     };
     auto read_scales = [&](int stage) {
         const uint8_t* from = lds + stage * STAGE + SCALES;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) sa[j] = *reinterpret_cast<const float*>(from + ((wm * MT + j) * 16 + c) * 4);
+        sa = *reinterpret_cast<const RowScales*>(from + (wm * 16 + c) * MT * 4);
         sw = *reinterpret_cast<const float*>(from + (A_SLOTS * kSlots + wn * NT * 16 / kFp8Block) * 4);
     };
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
-    load_weights(STAGES - 1);
-    load_rows(STAGES - 1);
+    load_first(STAGES - 1);
+    load_second(STAGES - 1);
     read_scales(0);
 #pragma unroll
     for (int j = 0; j < MT; ++j) x[j] = read_operand(x_base + j * 16 * kStepBytes);
     w[0] = read_operand(w_base);
+    w[1] = read_operand(w_base + 16 * kStepBytes);
     int stage = 0;
     while (load_tile.n > 0) {
         const TileItem tile = load_tile;
@@ -281,59 +315,83 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
         for (int s = 0; s < steps; ++s) {
             const int next = stage + 1 == STAGES ? 0 : stage + 1;
             float f[MT];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) f[j] = sa[j] * sw;
-            // product t's multiply-adds run behind product t + LAG
+            // A product's multiply-adds run behind the product LAG further on.  Products are counted in the order of
+            // their issue: block by block, the last two blocks row by row.
             constexpr int LAG = 2, COUNT = NT * MT;
             f32x4 p[LAG + 1];
             auto add = [&](auto t) {
-                constexpr int i = decltype(t)::value / MT, j = decltype(t)::value % MT;
+                constexpr int n = decltype(t)::value, tail = n - (NT - 2) * MT;
+                constexpr int i = tail < 0 ? n / MT : NT - 2 + tail % 2, j = tail < 0 ? n % MT : tail / 2;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(f[j], p[decltype(t)::value % (LAG + 1)][q], acc[i][j][q]);
+                for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(f[j], p[n % (LAG + 1)][q], acc[i][j][q]);
                 asm volatile("" : "+v"(acc[i][j]));
             };
-            auto product = [&](auto t) {
-                constexpr int n = decltype(t)::value, i = n / MT, j = n % MT;
-                p[n % (LAG + 1)] = block_product(w[i & 1], x[j]);
-                asm volatile("" : "+v"(p[n % (LAG + 1)]));  // in this place
+            auto product = [&](auto t, auto i, auto j) {
+                constexpr int n = decltype(t)::value;
+                p[n % (LAG + 1)] = block_product(w[decltype(i)::value % W_BUFFERS], x[decltype(j)::value]);
+                asm volatile("" : "+v"(p[n % (LAG + 1)]));
+                __builtin_amdgcn_sched_barrier(0);  // the product first, or its issue waits for the one that is added
+                if constexpr (n == LAG) {
+#pragma unroll
+                    for (int q = 0; q < MT; ++q) f[q] = sa[q] * sw;
+                }
                 if constexpr (n >= LAG) add(std::integral_constant<int, n - LAG>{});
+                __builtin_amdgcn_sched_barrier(0);
             };
             auto read_row = [&](auto j) { x[j] = read_operand(next * STAGE + x_base + j * 16 * kStepBytes); };
-            static_for<0, NT>([&](auto row) {
-                constexpr int i = decltype(row)::value;
-                if constexpr (i + 1 < NT) {
-                    w[(i + 1) & 1] = read_operand(stage * STAGE + w_base + (i + 1) * 16 * kStepBytes);
-                } else {
-                    // the next step has landed once no more than the loads behind it are left
-                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS) : "memory");
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                    read_scales(next);
-                    w[0] = read_operand(next * STAGE + w_base);
-                    if (load_step == steps) {
-                        start_tile();
-                        start_rows();
-                    }
-                    load_weights(stage);
-                    load_rows(stage);
+            // Everything read so far is in registers: the rows' place and half of the weights' are free.
+            auto first_half = [&]() {
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                if (load_step == steps) {
+                    start_tile();
+                    start_rows();
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                if (active) {
-                    static_for<0, MT>([&](auto column) {
-                        constexpr int j = decltype(column)::value;
-                        product(std::integral_constant<int, i * MT + j>{});
-                        if constexpr (i + 1 == NT) read_row(column);
-                    });
-                } else if constexpr (i + 1 == NT) {
-                    static_for<0, MT>(read_row);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
+                load_first(stage);
+            };
+            // The rest is read, and the next step has landed once no more than the loads behind it are left.
+            auto second_half = [&]() {
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS + FIRST) : "memory");
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                load_second(stage);
+            };
             if (active) {
+                auto read_weight = [&](auto i, int from, int n) { w[decltype(i)::value % W_BUFFERS] = read_operand(from * STAGE + w_base + n * 16 * kStepBytes); };
+                static_for<0, NT - 2>([&](auto row) {
+                    constexpr int i = decltype(row)::value;
+                    if constexpr (i == NT / 2 - 1) first_half();
+                    read_weight(std::integral_constant<int, i + 2>{}, stage, i + 2);
+                    __builtin_amdgcn_sched_barrier(0);
+                    static_for<0, MT>([&](auto column) { product(std::integral_constant<int, i * MT + decltype(column)::value>{}, row, column); });
+                });
+                if constexpr (NT == 2) first_half();
+                second_half();
+                // The last two blocks' products by rows, so that a row's operand is read for the next step as early
+                // as can be: the wavefronts' reads come all at once here.
+                if constexpr (NT > 2) read_weight(std::integral_constant<int, NT>{}, next, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                static_for<0, MT>([&](auto column) {
+                    constexpr int j = decltype(column)::value, n = (NT - 2) * MT + 2 * j;
+                    product(std::integral_constant<int, n>{}, std::integral_constant<int, NT - 2>{}, column);
+                    product(std::integral_constant<int, n + 1>{}, std::integral_constant<int, NT - 1>{}, column);
+                    read_row(column);
+                });
+                if constexpr (NT == 2) read_weight(std::integral_constant<int, NT>{}, next, 0);
+                read_weight(std::integral_constant<int, NT + 1>{}, next, 1);
+                __builtin_amdgcn_sched_barrier(0);
                 static_for<COUNT - LAG, COUNT>([&](auto t) { add(t); });
+                read_scales(next);  // behind the last use of this step's
+            } else {
+                first_half();
+                second_half();
+                read_scales(next);
+                w[0] = read_operand(next * STAGE + w_base);
+                w[1] = read_operand(next * STAGE + w_base + 16 * kStepBytes);
+                static_for<0, MT>(read_row);
             }
             stage = next;
         }
         find_tile(offset_of);
+        const int lane = lane_now();
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             const int m0 = (wm * MT + j) * 16;
