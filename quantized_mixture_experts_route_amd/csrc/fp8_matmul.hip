@@ -69,17 +69,21 @@ constexpr int kSlots = kWave;          // scales a wavefront loads in a step
 struct Span {
     const uint8_t* base;
     uint32_t bytes;
-    // Uniform, which the compiler does not see of what came out of LDS or through a multiplication on the
-    // vector units: without readfirstlane each load runs in a loop over its lanes' descriptors (8192 x 28672
-    // x 4096 over 8 experts: 1073 -> TODO us).
     __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
     {
-        const uint64_t p = (uint64_t)(base + at);
-        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
-        return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0,
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0,
                                                  __builtin_amdgcn_readfirstlane(mx_bytes_left(bytes, at)), 0x00020000);
     }
 };
+
+// A span in scalar registers.  It is uniform, which the compiler does not see of what came out of LDS or through
+// a product on the vector units; each load would run in a loop over its lanes' descriptors.
+__device__ inline Span uniform_span(const void* base, uint32_t bytes)
+{
+    const uint64_t p = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+    return Span{(const uint8_t*)((uint64_t)hi << 32 | lo), (uint32_t)__builtin_amdgcn_readfirstlane(bytes)};
+}
 
 // The lane, worked out where it stands.  What is made from it needs no register over the K loop; what the
 // compiler keeps there is spilled, and a reload waits for every load and store before it.
@@ -201,16 +205,16 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
         const bool on = t.n > 0;
         const int w_rows = on ? min(BN, a.N - t.n0) : 0;
         const int64_t w0 = on ? (int64_t)t.expert * a.N + t.n0 : 0;
-        w_span = Span{a.w_codes + w0 * K, (uint32_t)(w_rows * K)};
+        w_span = uniform_span(a.w_codes + w0 * K, (uint32_t)(w_rows * K));
         const int64_t a0 = a.sorted_routes ? 0 : t.row0;
         const int64_t a_rows = !on ? 0 : a.sorted_routes ? a.a_rows : t.n;
-        a_span = Span{a.a_codes + a0 * K, (uint32_t)(a_rows * K)};
+        a_span = uniform_span(a.a_codes + a0 * K, (uint32_t)(a_rows * K));
         if (wave < A_SLOTS) {
-            scale_span = Span{(const uint8_t*)(a.a_scales + a0 * blocks), (uint32_t)(a_rows * blocks * 4)};
+            scale_span = uniform_span(a.a_scales + a0 * blocks, (uint32_t)(a_rows * blocks * 4));
         } else {
             const int64_t s0 = on ? (int64_t)t.expert * n_blocks + t.n0 / kFp8Block : 0;
             const int rows = on && wave == A_SLOTS ? min(N_BLOCKS, n_blocks - t.n0 / kFp8Block) : 0;
-            scale_span = Span{(const uint8_t*)(a.w_scales + s0 * blocks), (uint32_t)(rows * blocks * 4)};
+            scale_span = uniform_span(a.w_scales + s0 * blocks, (uint32_t)(rows * blocks * 4));
             const int lane = lane_now();
             scale_at = lane < rows ? lane * (uint32_t)blocks * 4 : kMxOutside;
         }
@@ -231,48 +235,42 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     };
     // The weights' halves: rows that a wavefront's first and last NT / 2 blocks read, 8 WAVES rows in turn.
     static_assert(NT * 8 == 8 * WAVES, "a load of all wavefronts covers half of one's columns");
-    auto load_weights = [&](int stage, int half) {
+    // The loads of a step, one by one: scales, rows, the first halves of the weights (FIRST of them), the second halves.
+    auto load = [&](int stage, int q) {
         const uint32_t at = (uint32_t)load_step * kStepBytes;
-        const __amdgpu_buffer_rsrc_t buf = w_span.from(at);
-        const uint32_t row = w_at(lane_now());
-        const bool in = WHOLE || at + load_chunk(lane_now()) < (uint32_t)K;
-#pragma unroll
-        for (int j = half; j < LOADS_W; j += 2) {
-            load_to_lds<16>(buf, in ? row + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
-                            lds + stage * STAGE + (BM + (j * WAVES + wave) * 8) * kStepBytes);
+        uint8_t* const to = lds + stage * STAGE;
+        if (q == 0) {
+            load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside, to + SCALES + wave * kSlots * 4);
+            return;
+        }
+        const int lane = lane_now();
+        const bool in = WHOLE || at + load_chunk(lane) < (uint32_t)K;
+        if (q <= LOADS_A) {
+            const int j = q - 1;
+            load_to_lds<16>(a_span.from(at), in ? code_at[j] : kMxOutside, to + (j * WAVES + wave) * 8 * kStepBytes);
+        } else {
+            const int j = q < FIRST ? 2 * (q - 1 - LOADS_A) : 2 * (q - FIRST) + 1;
+            load_to_lds<16>(w_span.from(at), in ? w_at(lane) + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
+                            to + (BM + (j * WAVES + wave) * 8) * kStepBytes);
         }
     };
-    auto load_rows = [&](int stage) {  // and all scales
-        const uint32_t at = (uint32_t)load_step * kStepBytes;
-        const __amdgpu_buffer_rsrc_t buf = a_span.from(at);
-        const bool in = WHOLE || at + load_chunk(lane_now()) < (uint32_t)K;
-#pragma unroll
-        for (int j = 0; j < LOADS_A; ++j) {
-            load_to_lds<16>(buf, in ? code_at[j] : kMxOutside, lds + stage * STAGE + (j * WAVES + wave) * 8 * kStepBytes);
-        }
-        load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside,
-                       lds + stage * STAGE + SCALES + wave * kSlots * 4);
+    auto load_all = [&](int stage, auto from, auto to) {
+        static_for<decltype(from)::value, decltype(to)::value>([&](auto q) { load(stage, q); });
     };
-    auto load_first = [&](int stage) {
-        load_rows(stage);
-        load_weights(stage, 0);
-    };
-    auto load_second = [&](int stage) {
-        load_weights(stage, 1);
-        ++load_step;
-    };
+    constexpr std::integral_constant<int, 0> kNone;
+    constexpr std::integral_constant<int, 1 + LOADS_A> kWeights;
+    constexpr std::integral_constant<int, LOADS> kAll;
     find_tile([&](int e) { return __builtin_amdgcn_readfirstlane(scratch[e]); });
     start_tile();
-    load_weights(0, 0);  // weights do not wait for the table of rows
-    load_weights(0, 1);
+    load_all(0, kWeights, kAll);  // weights do not wait for the table of rows
     __syncthreads();
     start_rows();
-    load_rows(0);
+    load_all(0, kNone, kWeights);
     ++load_step;
 #pragma unroll
     for (int i = 1; i < STAGES - 1; ++i) {
-        load_first(i);
-        load_second(i);
+        load_all(i, kNone, kAll);
+        ++load_step;
     }
     find_tile(offset_of);
 
@@ -294,8 +292,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
         sw = *reinterpret_cast<const float*>(from + (A_SLOTS * kSlots + wn * NT * 16 / kFp8Block) * 4);
     };
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * LOADS) : "memory");
-    load_first(STAGES - 1);
-    load_second(STAGES - 1);
+    load_all(STAGES - 1, kNone, kAll);
+    ++load_step;
     read_scales(0);
 #pragma unroll
     for (int j = 0; j < MT; ++j) x[j] = read_operand(x_base + j * 16 * kStepBytes);
@@ -339,31 +337,44 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
                 __builtin_amdgcn_sched_barrier(0);
             };
             auto read_row = [&](auto j) { x[j] = read_operand(next * STAGE + x_base + j * 16 * kStepBytes); };
-            // Everything read so far is in registers: the rows' place and half of the weights' are free.
+            // The rows and the first halves of the weights are in registers: their places take the loads of the
+            // step STAGES ahead.
             auto first_half = [&]() {
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 if (load_step == steps) {
                     start_tile();
                     start_rows();
                 }
-                load_first(stage);
             };
             // The rest is read, and the next step has landed once no more than the loads behind it are left.
             auto second_half = [&]() {
                 asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * LOADS + FIRST) : "memory");
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                load_second(stage);
             };
             if (active) {
                 auto read_weight = [&](auto i, int from, int n) { w[decltype(i)::value % W_BUFFERS] = read_operand(from * STAGE + w_base + n * 16 * kStepBytes); };
+                // Loads are spread over the products (all at once they hold up the wavefront: 14336 inputs, 4096
+                // outputs, 8192 rows over 8 experts: 672 -> TODO us).
+                constexpr int MID = NT / 2 - 2, PLACES = (NT - 2 - MID) * MT;
                 static_for<0, NT - 2>([&](auto row) {
                     constexpr int i = decltype(row)::value;
-                    if constexpr (i == NT / 2 - 1) first_half();
+                    if constexpr (i == MID) first_half();
                     read_weight(std::integral_constant<int, i + 2>{}, stage, i + 2);
                     __builtin_amdgcn_sched_barrier(0);
-                    static_for<0, MT>([&](auto column) { product(std::integral_constant<int, i * MT + decltype(column)::value>{}, row, column); });
+                    static_for<0, MT>([&](auto column) {
+                        constexpr int j = decltype(column)::value, place = (i - MID) * MT + j;
+                        product(std::integral_constant<int, i * MT + j>{}, row, column);
+                        if constexpr (place >= 0) {
+                            static_for<0, FIRST>([&](auto q) {
+                                if constexpr (decltype(q)::value * PLACES / FIRST == place) load(stage, q);
+                            });
+                        }
+                    });
                 });
-                if constexpr (NT == 2) first_half();
+                if constexpr (NT == 2) {
+                    first_half();
+                    static_for<0, FIRST>([&](auto q) { load(stage, q); });
+                }
                 second_half();
                 // The last two blocks' products by rows, so that a row's operand is read for the next step as early
                 // as can be: the wavefronts' reads come all at once here.
@@ -374,6 +385,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
                     product(std::integral_constant<int, n>{}, std::integral_constant<int, NT - 2>{}, column);
                     product(std::integral_constant<int, n + 1>{}, std::integral_constant<int, NT - 1>{}, column);
                     read_row(column);
+                    static_for<FIRST, LOADS>([&](auto q) {
+                        if constexpr ((decltype(q)::value - FIRST) * MT / (LOADS - FIRST) == j) load(stage, q);
+                    });
                 });
                 if constexpr (NT == 2) read_weight(std::integral_constant<int, NT>{}, next, 0);
                 read_weight(std::integral_constant<int, NT + 1>{}, next, 1);
@@ -382,12 +396,15 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
                 read_scales(next);  // behind the last use of this step's
             } else {
                 first_half();
+                static_for<0, FIRST>([&](auto q) { load(stage, q); });
                 second_half();
+                static_for<FIRST, LOADS>([&](auto q) { load(stage, q); });
                 read_scales(next);
                 w[0] = read_operand(next * STAGE + w_base);
                 w[1] = read_operand(next * STAGE + w_base + 16 * kStepBytes);
                 static_for<0, MT>(read_row);
             }
+            ++load_step;
             stage = next;
         }
         find_tile(offset_of);
