@@ -35,34 +35,53 @@ __device__ inline uint64_t key_of(double c)
     return b >> 63 ? ~b : b | 1ull << 63;
 }
 
-__device__ inline uint64_t shfl_xor_u64(uint64_t v, int d)
+__device__ inline double value_of(uint64_t key)
 {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, d, kWave);
-    const uint32_t hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), d, kWave);
-    return (uint64_t)hi << 32 | lo;
-}
-
-struct Best {
-    uint64_t key;
-    int index;
-};
-
-// The wavefront's largest key, of equal ones the lowest index.
-__device__ inline Best wave_best(Best b)
-{
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const Best o{shfl_xor_u64(b.key, d), __shfl_xor(b.index, d, kWave)};
-        if (o.key > b.key || (o.key == b.key && o.index < b.index)) b = o;
-    }
-    return b;
+    return __builtin_bit_cast(double, key >> 63 ? key & ~(1ull << 63) : ~key);
 }
 
 __device__ inline double wave_sum_f64(double v)
 {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) v += __builtin_bit_cast(double, shfl_xor_u64(__builtin_bit_cast(uint64_t, v), d));
-    return v;
+    auto plus = [](double x, uint64_t o) { return x + __builtin_bit_cast(double, o); };
+    v = plus(v, dpp_u64<kDppXor1>(__builtin_bit_cast(uint64_t, v)));
+    v = plus(v, dpp_u64<kDppXor2>(__builtin_bit_cast(uint64_t, v)));
+    v = plus(v, dpp_u64<kDppHalfMirror>(__builtin_bit_cast(uint64_t, v)));
+    v = plus(v, dpp_u64<kDppMirror>(__builtin_bit_cast(uint64_t, v)));
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return plus(__builtin_bit_cast(double, readlane_u64(b, 0)), readlane_u64(b, 16)) +
+           plus(__builtin_bit_cast(double, readlane_u64(b, 32)), readlane_u64(b, 48));
+}
+
+// The largest two keys of two pairs.
+struct Two {
+    uint64_t first, second;
+};
+
+__device__ inline Two merge(Two a, Two b)
+{
+    const bool swap = b.first > a.first;
+    return Two{swap ? b.first : a.first, max_u64(swap ? a.first : b.first, swap ? b.second : a.second)};
+}
+
+// A group's rank as a key: the sum of its best one or two choices; 0 where all are masked.
+__device__ inline uint64_t rank_of(Two t, int group_top)
+{
+    if (group_top == 1 || t.second == 0 || t.first == ~0ull) return t.first;
+    return key_of(value_of(t.first) + value_of(t.second));
+}
+
+// The lane that holds the wavefront's largest key, the lowest of several (all of its bits: the high words
+// first, the low ones only where those tie); -1: no key is left.
+__device__ inline int wave_best(uint64_t key)
+{
+    const uint32_t hi = (uint32_t)(key >> 32), top = wave_max_u32(hi);
+    if (top == 0) return -1;  // only a masked choice's key has a high word of 0
+    uint64_t holders = __ballot(hi == top);
+    if (holders & (holders - 1)) {
+        const uint32_t lo = hi == top ? (uint32_t)key : 0u, low = wave_max_u32(lo);
+        holders = __ballot(hi == top && lo == low);
+    }
+    return __builtin_ctzll(holders);
 }
 
 // Sum over the chosen slots (lanes), in a fixed order.
@@ -83,79 +102,111 @@ __device__ inline float relative_score(bool sigmoid, float l, float m)
     return expf(fminf(l, 0.0f) - fminf(m, 0.0f)) * ((1.0f + expf(-fabsf(m))) / (1.0f + expf(-fabsf(l))));
 }
 
-// EPL experts a lane: expert lane + 64 j.
+// One wavefront a token, EPL neighbouring experts a lane: EPL * lane + j, so that the lowest lane of several
+// holds the lowest index.
+//
+// What bounds it: a chain of wavefront maxima, one for each slot, behind a float64 score for each expert.  TODO
 template <int DT, int EPL>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresArgs a)
 {
     typedef typename RowType<DT>::Raw Raw;
     __shared__ uint64_t choices[kWaves][EPL * kWave];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
     if (t >= a.T) return;  // the wavefronts of a workgroup do not meet
     const Raw* row = (const Raw*)a.logits + t * a.row_stride;
-    float l[EPL];
-    float m = -INFINITY;
-    bool nan = false;
+    const int e0 = lane * EPL;
+    float l[EPL], bias[EPL] = {};
+    if (e0 + EPL <= a.E) {
+        const auto x = load_vec<Raw, EPL>(row + e0);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane + kWave * j;
-        l[j] = e < a.E ? RowType<DT>::value(row[e]) : -INFINITY;
-        m = fmaxf(m, l[j]);
-        nan |= l[j] != l[j];
-    }
-    m = wave_max_f32(m);
-    const bool poisoned = !a.sigmoid && (__any(nan) || m == INFINITY);
-
-    double sum = 0.0;
-    double score[EPL];
+        for (int j = 0; j < EPL; ++j) l[j] = RowType<DT>::value(x.v[j]);
+        if (a.bias) {
+            const auto b = load_vec<float, EPL>(a.bias + e0);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        if (a.sigmoid) {
-            score[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-        } else {
-            score[j] = l[j] == -INFINITY ? 0.0 : poisoned ? (double)NAN : exp((double)l[j] - (double)m);
-            sum += score[j];
+            for (int j = 0; j < EPL; ++j) bias[j] = b.v[j];
         }
-    }
-    if (!a.sigmoid) sum = wave_sum_f64(sum);
-    uint64_t key[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane + kWave * j;
-        if (!a.sigmoid) score[j] /= sum;
-        const double c = a.bias && e < a.E ? score[j] + (double)a.bias[e] : score[j];
-        key[j] = l[j] == -INFINITY ? 0 : key_of(c);
-    }
-
-    if (a.top_groups < a.n_groups) {
-        const int size = a.E / a.n_groups;
-        for (int j = 0; j < EPL; ++j) choices[wave][lane + kWave * j] = key[j];
-        __builtin_amdgcn_wave_barrier();
-        // lane g ranks group g
-        uint64_t rank = 0;
-        if (lane < a.n_groups) {
-            uint64_t first = 0, second = 0;
-            for (int i = 0; i < size; ++i) {
-                const uint64_t k = choices[wave][lane * size + i];
-                second = max(second, min(first, k));
-                first = max(first, k);
-            }
-            rank = first;
-            if (a.group_top == 2 && second != 0 && first != ~0ull) {
-                auto value = [](uint64_t k) { return __builtin_bit_cast(double, k >> 63 ? k & ~(1ull << 63) : ~k); };
-                rank = key_of(value(first) + value(second));
-            }
-        }
-        uint64_t open = 0;
-        for (int i = 0; i < a.top_groups; ++i) {
-            const Best b = wave_best(Best{open >> lane & 1 ? 0 : rank, lane});
-            if (b.key == 0) break;
-            open |= 1ull << b.index;
-        }
+    } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const int e = lane + kWave * j;
-            if (e < a.E && !(open >> (e / size) & 1)) key[j] = 0;
+            l[j] = e0 + j < a.E ? RowType<DT>::value(row[e0 + j]) : -INFINITY;
+            if (a.bias && e0 + j < a.E) bias[j] = a.bias[e0 + j];
+        }
+    }
+    float m = -INFINITY;
+    double sum = 1.0;
+    bool poisoned = false;
+    double score[EPL];
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) score[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+    } else {
+        bool nan = false;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            m = fmaxf(m, l[j]);
+            nan |= l[j] != l[j];
+        }
+        m = wave_max_f32(m);
+        poisoned = __any(nan) || m == INFINITY;
+        double part = 0.0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            score[j] = l[j] == -INFINITY ? 0.0 : poisoned ? (double)NAN : exp((double)l[j] - (double)m);
+            part += score[j];
+        }
+        sum = wave_sum_f64(part);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) score[j] /= sum;
+    }
+    uint64_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : key_of(score[j] + (double)bias[j]);
+
+    if (a.top_groups < a.n_groups) {
+        const int size = a.E / a.n_groups, lanes = size / EPL;
+        if (size % EPL == 0 && (lanes & (lanes - 1)) == 0) {
+            // a group is `lanes` neighbouring lanes, a power of two of them
+            Two best{key[0], 0};
+#pragma unroll
+            for (int j = 1; j < EPL; ++j) best = merge(best, Two{key[j], 0});
+            if (lanes > 1) best = merge(best, Two{dpp_u64<kDppXor1>(best.first), dpp_u64<kDppXor1>(best.second)});
+            if (lanes > 2) best = merge(best, Two{dpp_u64<kDppXor2>(best.first), dpp_u64<kDppXor2>(best.second)});
+            if (lanes > 4) best = merge(best, Two{dpp_u64<kDppHalfMirror>(best.first), dpp_u64<kDppHalfMirror>(best.second)});
+            if (lanes > 8) best = merge(best, Two{dpp_u64<kDppMirror>(best.first), dpp_u64<kDppMirror>(best.second)});
+            for (int d = 16; d < lanes; d <<= 1) {
+                best = merge(best, Two{(uint64_t)__shfl_xor((unsigned long long)best.first, d, kWave),
+                                       (uint64_t)__shfl_xor((unsigned long long)best.second, d, kWave)});
+            }
+            const uint64_t rank = rank_of(best, a.group_top);
+            int before = 0;  // groups ahead of the lane's
+            for (int g = 0; g < a.n_groups; ++g) {
+                const uint64_t other = readlane_u64(rank, g * lanes);
+                before += other > rank || (other == rank && g * lanes < lane / lanes * lanes);
+            }
+            if (before >= a.top_groups || rank == 0) {
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) key[j] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) choices[wave][e0 + j] = key[j];
+            __builtin_amdgcn_wave_barrier();
+            Two best{0, 0};  // lane g's group is g
+            if (lane < a.n_groups) {
+                for (int i = 0; i < size; ++i) best = merge(best, Two{choices[wave][lane * size + i], 0});
+            }
+            const uint64_t rank = rank_of(best, a.group_top);
+            int before = 0;
+            for (int g = 0; g < a.n_groups; ++g) {
+                const uint64_t other = readlane_u64(rank, g);
+                before += other > rank || (other == rank && g < lane);
+            }
+            const uint64_t open = __ballot(lane < a.n_groups && before < a.top_groups && rank != 0);
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                if (e0 + j < a.E && !(open >> ((e0 + j) / size) & 1)) key[j] = 0;
+            }
         }
     }
 
@@ -163,25 +214,28 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
     int id = -1;
     float chosen = -INFINITY;  // its logit
     for (int s = 0; s < a.top_k; ++s) {
-        Best b{0, a.E};
+        uint64_t best = key[0];
+        int at = 0;
+        float logit = l[0];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (key[j] > b.key) b = Best{key[j], lane + kWave * j};
-        }
-        b = wave_best(b);
-        if (b.key == 0) break;
-        float v = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (lane + kWave * j == b.index) {
-                key[j] = 0;
-                v = l[j];
+        for (int j = 1; j < EPL; ++j) {
+            if (key[j] > best) {
+                best = key[j];
+                at = j;
+                logit = l[j];
             }
         }
-        v = __shfl(v, b.index % kWave, kWave);
+        const int from = wave_best(best);
+        if (from < 0) break;
+        const int e = from * EPL + __builtin_amdgcn_readlane(at, from);
+        const float v = readlane_f32(logit, from);
         if (lane == s) {
-            id = b.index;
+            id = e;
             chosen = v;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (e0 + j == e) key[j] = 0;
         }
     }
     float w = 0.0f;
