@@ -16,7 +16,7 @@
 // need the operands as f16 at half the rate, and are refused.
 #include "expert_tiles.h"
 #include "fp8_ops.h"
-#include "mx_shape.h"
+#include "fp8_shape.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {
@@ -104,6 +104,22 @@ __device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lane_offse
     else __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 4, lane_offset, 0, 0, 0);
 }
 
+// Rows behind the last expert's are zero; `end` is the last offset.
+template <int THREADS>
+__device__ inline void clear_behind(const Fp8MatmulArgs& a, int end)
+{
+    if (!a.offsets) return;
+    uint16_t* const out = (uint16_t*)a.out;
+    const int64_t lo = (int64_t)min(max(end, 0), a.rows) * a.N, hi = (int64_t)a.rows * a.N;
+    for (int64_t i = lo + (blockIdx.x * (int64_t)THREADS + threadIdx.x) * 8; i < hi; i += (int64_t)gridDim.x * THREADS * 8) {
+        if (i + 8 <= hi) {
+            store_vec<uint16_t, 8>(out + i, RowVec<uint16_t, 8>{});
+        } else {
+            for (int64_t q = i; q < hi; ++q) out[q] = 0;
+        }
+    }
+}
+
 // Stores two neighbouring blocks of 16 x 16 results: lane 16 g + c holds row c, columns 4 g + i of either in
 // register i.  `out` is the first row and column; rows and cols say how many of them exist (WHOLE: all).
 template <int DT, bool WHOLE>
@@ -160,17 +176,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     const int end = (int)((int64_t)total * (die + 1) / 8);
     int next_item = (int)((int64_t)total * die / 8) + blockIdx.x / 8;
 
-    // rows behind the last expert's are zero
-    if (a.offsets) {
-        const int64_t lo = (int64_t)min(max(a.offsets[a.E], 0), a.rows) * a.N, hi = (int64_t)a.rows * a.N;
-        for (int64_t i = lo + (blockIdx.x * (int64_t)THREADS + threadIdx.x) * 8; i < hi; i += (int64_t)gridDim.x * THREADS * 8) {
-            if (i + 8 <= hi) {
-                store_vec<uint16_t, 8>((uint16_t*)a.out + i, RowVec<uint16_t, 8>{});
-            } else {
-                for (int64_t q = i; q < hi; ++q) ((uint16_t*)a.out)[q] = 0;
-            }
-        }
-    }
+    clear_behind<THREADS>(a, a.offsets ? a.offsets[a.E] : 0);
 
     // ---- the loading side: an item and a step, up to STAGES steps ahead
     TileItem load_tile;
@@ -424,15 +430,110 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may reach LDS behind the workgroup's end
 }
 
+// ---------------------------------------------------------------- few rows
+// Up to 16 rows against 32 weight rows; the eight wavefronts share K block by block, operands straight from
+// memory, every load of four blocks a wavefront under way at once.  Their sums meet in LDS, in the order of the
+// wavefronts.  For products of few tiles, which are a chain of latencies: the tiled kernel walks K step by step.
+constexpr int kRowsWaves = 8, kRowsTile = 16, kRowsColumns = 32, kRowsAhead = 4;
+
+template <int DT>
+__global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
+{
+    constexpr int THREADS = 64 * kRowsWaves, PITCH = kRowsColumns + 4;
+    __shared__ int first[kMaxExperts + 1], scratch[kMaxExperts + 1];
+    __shared__ __align__(16) float sums[kRowsWaves][kRowsTile][PITCH];
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int K = a.K, blocks = (K + kFp8Block - 1) / kFp8Block, n_blocks = (a.N + kFp8Block - 1) / kFp8Block;
+    build_tile_list<kRowsTile, THREADS>(first, scratch, a.offsets, a.E, a.rows);
+    const int n_tiles = (a.N + kRowsColumns - 1) / kRowsColumns;
+    const int total = __builtin_amdgcn_readfirstlane(mx_items(first[a.E], n_tiles, a.rows, kRowsTile, a.E));
+    clear_behind<THREADS>(a, scratch[a.E]);
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const TileItem t = item_at<kRowsTile, kRowsColumns>(
+            first, [&](int e) { return __builtin_amdgcn_readfirstlane(scratch[e]); }, a.E, n_tiles, item, total);
+        int source = min(c, t.n - 1);  // from the tile's first row where there are no routes
+        if (a.sorted_routes) {
+            const int route = a.sorted_routes[t.row0 + source];
+            source = route < 0 || route / a.top_k >= a.a_rows ? -1 : route / a.top_k;
+        }
+        const int64_t a0 = a.sorted_routes ? 0 : t.row0, a_rows = a.sorted_routes ? a.a_rows : t.n;
+        const int64_t w0 = (int64_t)t.expert * a.N + t.n0;
+        const int w_rows = min(kRowsColumns, a.N - t.n0);
+        const Span x_span{a.a_codes + a0 * K, (uint32_t)(a_rows * K)}, w_span{a.w_codes + w0 * K, (uint32_t)(w_rows * K)};
+        const Span sx_span{(const uint8_t*)(a.a_scales + a0 * blocks), (uint32_t)(a_rows * blocks * 4)};
+        const float* const sw_row = a.w_scales + ((int64_t)t.expert * n_blocks + t.n0 / kFp8Block) * blocks;
+        const uint32_t x_at = source < 0 ? kMxOutside : source * (uint32_t)K, sx_at = source < 0 ? kMxOutside : source * (uint32_t)blocks * 4;
+        const uint32_t w_at = c * (uint32_t)K;  // rows behind N: out of bounds
+        f32x4 acc[2] = {};
+        for (int b0 = wave; b0 < blocks; b0 += kRowsWaves * kRowsAhead) {
+            u32x4 x[kRowsAhead][2], w[kRowsAhead][2][2];
+            float sx[kRowsAhead], sw[kRowsAhead];
+#pragma unroll
+            for (int q = 0; q < kRowsAhead; ++q) {
+                const int b = b0 + q * kRowsWaves;
+                const bool there = b < blocks;
+                const uint32_t at = there ? (uint32_t)b * kStepBytes : 0;
+                const auto xr = x_span.from(at), wr = w_span.from(at);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // chunks g and g + 4, as in the tiled kernel
+                    const uint32_t k = (g + 4 * h) * 16;
+                    const bool in = there && at + k < (uint32_t)K;
+                    x[q][h] = __builtin_amdgcn_raw_buffer_load_b128(xr, in && source >= 0 ? x_at + k : kMxOutside, 0, 0);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        w[q][n][h] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? w_at + (uint32_t)(n * 16) * K + k : kMxOutside, 0, 0);
+                    }
+                }
+                sx[q] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sx_span.from(there ? b * 4 : 0), there ? sx_at : kMxOutside, 0, 0));
+                sw[q] = there ? sw_row[b] : 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < kRowsAhead; ++q) {
+                const float f = sx[q] * sw[q];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const f32x4 p = block_product(operand(w[q][n][0], w[q][n][1]), operand(x[q][0], x[q][1]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f, p[i], acc[n][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) *reinterpret_cast<f32x4*>(&sums[wave][c][n * 16 + g * 4]) = acc[n];
+        __syncthreads();
+        const int row = threadIdx.x / kRowsColumns, column = threadIdx.x % kRowsColumns;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRowsWaves; ++i) sum += sums[i][row][column];
+        if (row < t.n && t.n0 + column < a.N) {
+            ((uint16_t*)a.out)[(int64_t)(t.row0 + row) * a.N + t.n0 + column] = Dt<DT>::from_float(sum);
+        }
+        __syncthreads();
+    }
+}
+
+// At most one partial tile for every expert with rows.
+int64_t most_items(const Fp8MatmulArgs& a, int bm, int bn)
+{
+    const int64_t experts = a.E < a.rows ? a.E : a.rows;
+    return (experts + (a.rows - experts) / bm) * ((a.N + bn - 1) / bn);
+}
+
+template <int DT>
+hipError_t launch_rows(const Fp8MatmulArgs& a, hipStream_t s)
+{
+    const int64_t items = most_items(a, kRowsTile, kRowsColumns);
+    launch(rows_kernel<DT>, dim3((unsigned)(items < 2 * kMxCUs ? items : 2 * kMxCUs)), dim3(64 * kRowsWaves), s, a);
+    return hipGetLastError();
+}
+
 // wgs_per_cu: as many as fit by LDS and registers.
 template <int DT, int MT, int NT, int WM, int WN, int STAGES>
 hipError_t launch_tiled(const Fp8MatmulArgs& a, int wgs_per_cu, hipStream_t s)
 {
     constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN;
-    // at most one partial tile for every expert with rows
-    const int64_t experts = a.E < a.rows ? a.E : a.rows;
-    const int64_t items = (experts + (a.rows - experts) / BM) * ((a.N + BN - 1) / BN);
-    int64_t grid = (items + 7) / 8 * 8;
+    int64_t grid = (most_items(a, BM, BN) + 7) / 8 * 8;
     if (grid > kMxCUs * wgs_per_cu) grid = kMxCUs * wgs_per_cu;
     const dim3 threads(64 * WM * WN);
     if (a.K % kFp8Block == 0 && a.K / kFp8Block >= STAGES) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), threads, s, a);
@@ -443,13 +544,12 @@ hipError_t launch_tiled(const Fp8MatmulArgs& a, int wgs_per_cu, hipStream_t s)
 template <int DT>
 hipError_t launch_by_shape(const Fp8MatmulArgs& a, hipStream_t s)
 {
-    switch (mx_tile(a.E, a.N, a.K, a.rows)) {
-    case MxTile::k32x64s4: return launch_tiled<DT, 2, 2, 1, 2, 4>(a, 2, s);
-    case MxTile::k64x128s4: return launch_tiled<DT, 2, 4, 2, 2, 4>(a, 1, s);
-    case MxTile::k128x128s4: return launch_tiled<DT, 4, 4, 2, 2, 4>(a, 1, s);
-    case MxTile::k64x128s2: return launch_tiled<DT, 2, 4, 2, 2, 2>(a, 2, s);
-    case MxTile::k128x128s2: return launch_tiled<DT, 4, 4, 2, 2, 2>(a, 2, s);
-    case MxTile::k256x256s2: break;
+    switch (fp8_tile(a.E, a.N, a.rows)) {
+    case Fp8Tile::kRows: return launch_rows<DT>(a, s);
+    case Fp8Tile::k32x64s4: return launch_tiled<DT, 2, 2, 1, 2, 4>(a, 2, s);
+    case Fp8Tile::k64x128s3: return launch_tiled<DT, 2, 4, 2, 2, 3>(a, 2, s);
+    case Fp8Tile::k128x128s2: return launch_tiled<DT, 4, 4, 2, 2, 2>(a, 2, s);
+    case Fp8Tile::k256x256s2: break;
     }
     return launch_tiled<DT, 4, 8, 4, 2, 2>(a, 1, s);
 }
