@@ -72,7 +72,7 @@ struct Span {
     __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
     {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0,
-                                                 __builtin_amdgcn_readfirstlane(mx_bytes_left(bytes, at)), 0x00020000);
+                                                 mx_bytes_left(__builtin_amdgcn_readfirstlane(bytes), at), 0x00020000);
     }
 };
 
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     int load_step = 0;
     auto load_chunk = [&](int lane) { return (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16; };
     uint32_t code_at[LOADS_A];  // byte offset of the lane's chunk at step 0
-    auto w_at = [&](int lane) { return (wave * 8 + (lane >> 3)) * (uint32_t)K + load_chunk(lane); };  // rows behind N: out of bounds
+    const uint32_t w_row = (wave * 8 + (lane_now() >> 3)) * (uint32_t)K + load_chunk(lane_now());  // rows behind N: out of bounds
     uint32_t scale_at;          // byte offset of the lane's scale at step 0
     Span a_span, w_span, scale_span;
     // The next item, found between two tiles, where registers are free; and in LDS its rows' source rows in a
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
             load_to_lds<16>(a_span.from(at), in ? code_at[j] : kMxOutside, to + (j * WAVES + wave) * 8 * kStepBytes);
         } else {
             const int j = q < FIRST ? 2 * (q - 1 - LOADS_A) : 2 * (q - FIRST) + 1;
-            load_to_lds<16>(w_span.from(at), in ? w_at(lane) + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
+            load_to_lds<16>(w_span.from(at), in ? opaque(w_row) + (uint32_t)(j * WAVES * 8) * K : kMxOutside,
                             to + (BM + (j * WAVES + wave) * 8) * kStepBytes);
         }
     };
