@@ -132,7 +132,7 @@ def _cpu_baseline(inp, spec, min_seconds):
 # Sources of the operators beside the layer: none of the layer's kernels includes them.
 OTHER_OPERATORS = ("expert_ops.cpp", "expert_ops.h", "permute.hip", "mx_convert.hip", "mx_matmul.hip", "mx_shape.h",
                    "rowio.h", "abi_checks.h", "expert_tiles.h", "fp8_ops.cpp", "fp8_ops.h", "route_scores.hip",
-                   "fp8_block.h", "fp8_shape.h", "fp8_convert.hip", "fp8_matmul.hip", "activate.hip")
+                   "fp8_block.h", "fp8_shape.h", "logistic.h", "fp8_convert.hip", "fp8_matmul.hip", "activate.hip")
 
 
 def kernel_source_digest():

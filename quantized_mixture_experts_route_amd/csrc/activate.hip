@@ -15,32 +15,13 @@
 #include <algorithm>
 
 #include "fp8_block.h"
+#include "logistic.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {
 namespace {
 
 constexpr int kThreads = 256;
-
-// s(z) and s(-z) = 1 - s(z), each to a few units of float32: the exponential's argument z log2(e) is
-// carried in two parts, since its rounding error would grow with |z|.
-struct Logistic {
-    float s, rest;
-};
-
-__device__ inline Logistic logistic(float z)
-{
-    constexpr float kLog2E = 1.44269502f, kLog2ERest = 1.92596299e-8f, kLn2 = 0.693147182f;
-    const float a = fabsf(z);
-    const float hi = a * kLog2E, lo = fmaf(a, kLog2E, -hi) + a * kLog2ERest;
-    // past 2^-150 the exponential is 0, and lo may be inf - inf there
-    const float e = hi < 150.0f ? __builtin_amdgcn_exp2f(-hi) * fmaf(lo, -kLn2, 1.0f) : 0.0f * a;
-    const float d = 1.0f + e;
-    float q = __builtin_amdgcn_rcpf(d);
-    q = fmaf(fmaf(-d, q, 1.0f), q, q);
-    const float eq = e * q;
-    return z >= 0.0f ? Logistic{q, eq} : Logistic{eq, q};
-}
 
 struct Pair {
     float gate, up;

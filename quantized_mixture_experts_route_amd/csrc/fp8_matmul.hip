@@ -360,7 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
             if (active) {
                 auto read_weight = [&](auto i, int from, int n) { w[decltype(i)::value % W_BUFFERS] = read_operand(from * STAGE + w_base + n * 16 * kStepBytes); };
                 // Loads are spread over the products (all at once they hold up the wavefront: 14336 inputs, 4096
-                // outputs, 8192 rows over 8 experts: 672 -> TODO us).
+                // outputs, 8192 rows over 8 experts: 672 -> 557 us).
                 constexpr int MID = NT / 2 - 2, PLACES = (NT - 2 - MID) * MT;
                 static_for<0, NT - 2>([&](auto row) {
                     constexpr int i = decltype(row)::value;

@@ -7,9 +7,10 @@
 // groups the top_k largest choices are taken, ties to the lower index.  Weights
 // are s at the chosen experts, divided by their sum (normalize), times scale.
 //
-// Choices are compared in float64: two experts whose choices differ by less than
-// float32 tells apart would change places from one implementation to the next,
-// and with them whole rows of the layer's output.
+// Choices are ordered as in float64 (in float32 first, again in float64 where that
+// is too near to tell): two experts whose choices differ by less than float32 tells
+// apart would change places from one implementation to the next, and with them
+// whole rows of the layer's output.
 //
 // Gradient, with G the gradient of the weights times scale and w the weights
 // before scale:
@@ -18,6 +19,7 @@
 //   softmax:               dl = s (G - sum G s), every expert (G 0 where not chosen)
 //   softmax, normalised:   dl = w (G - sum G w), the chosen experts
 #include "fp8_ops.h"
+#include "logistic.h"
 #include "qmoe_internal.h"
 #include "rowio.h"
 
@@ -102,10 +104,251 @@ __device__ inline float relative_score(bool sigmoid, float l, float m)
     return expf(fminf(l, 0.0f) - fminf(m, 0.0f)) * ((1.0f + expf(-fabsf(m))) / (1.0f + expf(-fabsf(l))));
 }
 
+// ---------------------------------------------------------------- the choice
 // One wavefront a token, EPL neighbouring experts a lane: EPL * lane + j, so that the lowest lane of several
-// holds the lowest index.
-//
-// What bounds it: a chain of wavefront maxima, one for each slot, behind a float64 score for each expert.  TODO
+// holds the lowest index.  Both forms leave slot s's expert in lane s (-1: none is left).
+
+// Choices in float32, and float64 where they come too near one another: two choices differ in float64 as they do
+// in float32 if they are further apart than kNear (1 + |choice|), or than kNear of it where there is no bias.  A
+// score in float32 is off by 8 units of 2^-24 (sigmoid) or 30 (softmax: the sum's rounding and that of l - m, whose
+// mean over the scores is below log E), a sum with a bias by one more; kNear is 64 units for the difference of two.
+// Choices in a chain of near ones, which may reach past the last slot, are put in order by their float64 values,
+// one a lane.  False where that does not do: groups that near one another at the last place, near choices by
+// softmax with a bias (their sum over all experts counts), groups of other sizes.
+constexpr float kNear = 0x1p-18f;
+
+__device__ inline uint32_t key32(float c)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, c + 0.0f);
+    return c == -INFINITY ? 0u : (int32_t)b < 0 ? ~b : b | 0x80000000u;
+}
+
+__device__ inline float value32(uint32_t key)
+{
+    return __builtin_bit_cast(float, (int32_t)key < 0 ? key & 0x7fffffffu : ~key);
+}
+
+struct Two32 {
+    uint32_t first, second;
+};
+
+__device__ inline Two32 merge(Two32 a, Two32 b)
+{
+    return Two32{max(a.first, b.first), max(min(a.first, b.first), max(a.second, b.second))};
+}
+
+template <int CTRL>
+__device__ inline Two32 merge_dpp(Two32 a)
+{
+    return merge(a, Two32{dpp_u32<CTRL>(a.first), dpp_u32<CTRL>(a.second)});
+}
+
+// Whether a group is a whole power of two of lanes.
+__device__ inline bool groups_fit(int size, int epl)
+{
+    const int lanes = size / epl;
+    return size % epl == 0 && (lanes & (lanes - 1)) == 0;
+}
+
+template <int EPL>
+__device__ inline bool choose_fast(const RouteScoresArgs& a, int lane, const float (&score)[EPL], const float (&bias)[EPL],
+                                   const float (&l)[EPL], float m, int& id)
+{
+    uint32_t key[EPL];
+    const float base = a.bias ? 1.0f : 0.0f;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const float c = score[j] + bias[j];
+        nan |= c != c;
+        key[j] = l[j] == -INFINITY ? 0u : key32(c);
+    }
+    if (__any(nan)) return false;
+    if (a.top_groups < a.n_groups) {
+        const int size = a.E / a.n_groups, lanes = size / EPL;
+        if (!groups_fit(size, EPL)) return false;
+        Two32 best{key[0], 0};
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) best = merge(best, Two32{key[j], 0});
+        if (lanes > 1) best = merge_dpp<kDppXor1>(best);
+        if (lanes > 2) best = merge_dpp<kDppXor2>(best);
+        if (lanes > 4) best = merge_dpp<kDppHalfMirror>(best);
+        if (lanes > 8) best = merge_dpp<kDppMirror>(best);
+        for (int d = 16; d < lanes; d <<= 1) {
+            best = merge(best, Two32{(uint32_t)__shfl_xor((int)best.first, d, kWave), (uint32_t)__shfl_xor((int)best.second, d, kWave)});
+        }
+        float rank = best.first ? value32(best.first) : -INFINITY, size_of = best.first ? fabsf(rank) : 0.0f;
+        if (a.group_top == 2 && best.second) {
+            rank += value32(best.second);
+            size_of += fabsf(value32(best.second));
+        }
+        const int mine = lane / lanes;
+        int before = 0;  // groups ahead of the lane's
+        for (int g = 0; g < a.n_groups; ++g) {
+            const float other = readlane_f32(rank, g * lanes);
+            before += other > rank || (other == rank && g < mine);
+        }
+        const bool in = mine < a.n_groups, kept = before < a.top_groups;
+        const float least = -wave_max_f32(in && kept ? -rank : -INFINITY), most = wave_max_f32(in && !kept ? rank : -INFINITY);
+        // a rank's error goes with what it is the sum of, which with a bias may be far larger than the rank;
+        // without an expert left in the best of the others nothing hangs on it (least - most is inf or NaN)
+        const float scale = a.bias ? 1.0f + wave_max_f32(size_of) : least;
+        if (least - most <= 4.0f * kNear * scale + 0x1p-120f) return false;
+        if (!kept) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) key[j] = 0;
+        }
+    }
+    float last = INFINITY, logit = -INFINITY;
+    bool in_doubt = false;
+    int n = 0;  // candidates, in lanes 0 .. n - 1
+    for (;; ++n) {
+        uint32_t top = key[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) top = max(top, key[j]);
+        const uint32_t mine = top;
+        top = wave_max_u32(top);
+        if (top == 0) break;
+        const float c = value32(top);
+        const bool near = last - c <= kNear * (base + fabsf(c));
+        if (n >= a.top_k && !near) break;
+        if (n == kWave) return false;
+        in_doubt |= near;
+        last = c;
+        const int from = __builtin_ctzll(__ballot(mine == top));
+        int here = EPL - 1;
+        float value = l[EPL - 1];
+#pragma unroll
+        for (int j = EPL - 2; j >= 0; --j) {
+            here = key[j] == top ? j : here;
+            value = key[j] == top ? l[j] : value;
+        }
+        const int e = from * EPL + __builtin_amdgcn_readlane(here, from);
+        value = readlane_f32(value, from);
+        if (lane == n) {
+            id = e;
+            logit = value;
+        }
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (lane * EPL + j == e) key[j] = 0;
+        }
+    }
+    if (in_doubt) {
+        if (!a.sigmoid && a.bias) return false;
+        // softmax without a bias: exp(l - m) orders as the scores do
+        const double score64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)logit)) : exp((double)logit - (double)m);
+        const uint64_t exact = id < 0 ? 0 : key_of(score64 + (a.bias ? (double)a.bias[id] : 0.0));
+        int before = 0;
+        for (int i = 0; i < n; ++i) {
+            const uint64_t other = readlane_u64(exact, i);
+            before += other > exact || (other == exact && __builtin_amdgcn_readlane(id, i) < id);
+        }
+        id = __builtin_amdgcn_ds_permute((lane < n ? before : lane) * 4, id);
+    }
+    if (lane >= a.top_k) id = -1;
+    return true;
+}
+
+// The same in float64, whatever the margins.  choices: EPL * 64 words of LDS.
+template <int EPL>
+__device__ inline int choose_exactly(const RouteScoresArgs& a, int lane, const float (&l)[EPL], const float (&bias)[EPL],
+                                     float m, bool poisoned, uint64_t* choices)
+{
+    const int e0 = lane * EPL;
+    double score[EPL];
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) score[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+    } else {
+        double part = 0.0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            score[j] = l[j] == -INFINITY ? 0.0 : poisoned ? (double)NAN : exp((double)l[j] - (double)m);
+            part += score[j];
+        }
+        const double sum = wave_sum_f64(part);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) score[j] /= sum;
+    }
+    uint64_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : key_of(score[j] + (double)bias[j]);
+
+    if (a.top_groups < a.n_groups) {
+        const int size = a.E / a.n_groups, lanes = size / EPL;
+        if (groups_fit(size, EPL)) {
+            Two best{key[0], 0};
+#pragma unroll
+            for (int j = 1; j < EPL; ++j) best = merge(best, Two{key[j], 0});
+            if (lanes > 1) best = merge(best, Two{dpp_u64<kDppXor1>(best.first), dpp_u64<kDppXor1>(best.second)});
+            if (lanes > 2) best = merge(best, Two{dpp_u64<kDppXor2>(best.first), dpp_u64<kDppXor2>(best.second)});
+            if (lanes > 4) best = merge(best, Two{dpp_u64<kDppHalfMirror>(best.first), dpp_u64<kDppHalfMirror>(best.second)});
+            if (lanes > 8) best = merge(best, Two{dpp_u64<kDppMirror>(best.first), dpp_u64<kDppMirror>(best.second)});
+            for (int d = 16; d < lanes; d <<= 1) {
+                best = merge(best, Two{(uint64_t)__shfl_xor((unsigned long long)best.first, d, kWave),
+                                       (uint64_t)__shfl_xor((unsigned long long)best.second, d, kWave)});
+            }
+            const uint64_t rank = rank_of(best, a.group_top);
+            int before = 0;  // groups ahead of the lane's
+            for (int g = 0; g < a.n_groups; ++g) {
+                const uint64_t other = readlane_u64(rank, g * lanes);
+                before += other > rank || (other == rank && g * lanes < lane / lanes * lanes);
+            }
+            if (before >= a.top_groups || rank == 0) {
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) key[j] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) choices[e0 + j] = key[j];
+            __builtin_amdgcn_wave_barrier();
+            Two best{0, 0};  // lane g's group is g
+            if (lane < a.n_groups) {
+                for (int i = 0; i < size; ++i) best = merge(best, Two{choices[lane * size + i], 0});
+            }
+            const uint64_t rank = rank_of(best, a.group_top);
+            int before = 0;
+            for (int g = 0; g < a.n_groups; ++g) {
+                const uint64_t other = readlane_u64(rank, g);
+                before += other > rank || (other == rank && g < lane);
+            }
+            const uint64_t open = __ballot(lane < a.n_groups && before < a.top_groups && rank != 0);
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) {
+                if (e0 + j < a.E && !(open >> ((e0 + j) / size) & 1)) key[j] = 0;
+            }
+        }
+    }
+
+    int id = -1;
+    for (int s = 0; s < a.top_k; ++s) {
+        uint64_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) {
+            if (key[j] > best) {
+                best = key[j];
+                at = j;
+            }
+        }
+        const int from = wave_best(best);
+        if (from < 0) break;
+        const int e = from * EPL + __builtin_amdgcn_readlane(at, from);
+        if (lane == s) id = e;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            if (e0 + j == e) key[j] = 0;
+        }
+    }
+    return id;
+}
+
+// What bounds it: few tokens, the launch and the chain of wavefront maxima, one for each slot; many, the
+// instructions of a token, about 800 (65536 tokens, 256 experts in 8 groups, top-8: 84 us for 72 MB; with every
+// choice in float64 102; 4096 tokens of 1024 experts, top-16: 24 us against 33).  A lane holds neighbouring experts
+// so that a group is a few lanes and its best two come by DPP; a wavefront a token, since a token's maxima are
+// then one reduction each and nothing waits at a barrier.
 template <int DT, int EPL>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresArgs a)
 {
@@ -133,13 +376,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
             if (a.bias && e0 + j < a.E) bias[j] = a.bias[e0 + j];
         }
     }
-    float m = -INFINITY;
-    double sum = 1.0;
+    float m = -INFINITY, sum = 1.0f;
     bool poisoned = false;
-    double score[EPL];
+    float score[EPL];
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) score[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+        for (int j = 0; j < EPL; ++j) score[j] = logistic(l[j]).s;
     } else {
         bool nan = false;
 #pragma unroll
@@ -149,95 +391,22 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
         }
         m = wave_max_f32(m);
         poisoned = __any(nan) || m == INFINITY;
-        double part = 0.0;
+        float part = 0.0f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            score[j] = l[j] == -INFINITY ? 0.0 : poisoned ? (double)NAN : exp((double)l[j] - (double)m);
+            score[j] = l[j] == -INFINITY ? 0.0f : exp_of(l[j] - m);
             part += score[j];
         }
-        sum = wave_sum_f64(part);
+        sum = wave_sum_f32(part);
+        const float inverse = 1.0f / sum;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) score[j] /= sum;
+        for (int j = 0; j < EPL; ++j) score[j] *= inverse;
     }
-    uint64_t key[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : key_of(score[j] + (double)bias[j]);
-
-    if (a.top_groups < a.n_groups) {
-        const int size = a.E / a.n_groups, lanes = size / EPL;
-        if (size % EPL == 0 && (lanes & (lanes - 1)) == 0) {
-            // a group is `lanes` neighbouring lanes, a power of two of them
-            Two best{key[0], 0};
-#pragma unroll
-            for (int j = 1; j < EPL; ++j) best = merge(best, Two{key[j], 0});
-            if (lanes > 1) best = merge(best, Two{dpp_u64<kDppXor1>(best.first), dpp_u64<kDppXor1>(best.second)});
-            if (lanes > 2) best = merge(best, Two{dpp_u64<kDppXor2>(best.first), dpp_u64<kDppXor2>(best.second)});
-            if (lanes > 4) best = merge(best, Two{dpp_u64<kDppHalfMirror>(best.first), dpp_u64<kDppHalfMirror>(best.second)});
-            if (lanes > 8) best = merge(best, Two{dpp_u64<kDppMirror>(best.first), dpp_u64<kDppMirror>(best.second)});
-            for (int d = 16; d < lanes; d <<= 1) {
-                best = merge(best, Two{(uint64_t)__shfl_xor((unsigned long long)best.first, d, kWave),
-                                       (uint64_t)__shfl_xor((unsigned long long)best.second, d, kWave)});
-            }
-            const uint64_t rank = rank_of(best, a.group_top);
-            int before = 0;  // groups ahead of the lane's
-            for (int g = 0; g < a.n_groups; ++g) {
-                const uint64_t other = readlane_u64(rank, g * lanes);
-                before += other > rank || (other == rank && g * lanes < lane / lanes * lanes);
-            }
-            if (before >= a.top_groups || rank == 0) {
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) key[j] = 0;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) choices[wave][e0 + j] = key[j];
-            __builtin_amdgcn_wave_barrier();
-            Two best{0, 0};  // lane g's group is g
-            if (lane < a.n_groups) {
-                for (int i = 0; i < size; ++i) best = merge(best, Two{choices[wave][lane * size + i], 0});
-            }
-            const uint64_t rank = rank_of(best, a.group_top);
-            int before = 0;
-            for (int g = 0; g < a.n_groups; ++g) {
-                const uint64_t other = readlane_u64(rank, g);
-                before += other > rank || (other == rank && g < lane);
-            }
-            const uint64_t open = __ballot(lane < a.n_groups && before < a.top_groups && rank != 0);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                if (e0 + j < a.E && !(open >> ((e0 + j) / size) & 1)) key[j] = 0;
-            }
-        }
-    }
-
-    // slot s is lane s's
     int id = -1;
-    float chosen = -INFINITY;  // its logit
-    for (int s = 0; s < a.top_k; ++s) {
-        uint64_t best = key[0];
-        int at = 0;
-        float logit = l[0];
-#pragma unroll
-        for (int j = 1; j < EPL; ++j) {
-            if (key[j] > best) {
-                best = key[j];
-                at = j;
-                logit = l[j];
-            }
-        }
-        const int from = wave_best(best);
-        if (from < 0) break;
-        const int e = from * EPL + __builtin_amdgcn_readlane(at, from);
-        const float v = readlane_f32(logit, from);
-        if (lane == s) {
-            id = e;
-            chosen = v;
-        }
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (e0 + j == e) key[j] = 0;
-        }
+    if (poisoned || !choose_fast<EPL>(a, lane, score, bias, l, m, id)) {
+        id = choose_exactly<EPL>(a, lane, l, bias, m, poisoned, choices[wave]);
     }
+    const float chosen = id >= 0 ? RowType<DT>::value(row[id]) : -INFINITY;
     float w = 0.0f;
     if (a.normalize) {
         const float top = wave_max_f32(chosen);  // NaN compares false and is skipped
@@ -245,7 +414,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
         const float total = sum_slots(r);
         if (id >= 0) w = r / total;
     } else if (id >= 0) {
-        w = a.sigmoid ? logistic_of(chosen) : expf(chosen - m) / (float)sum;
+        w = a.sigmoid ? logistic_of(chosen) : expf(chosen - m) / sum;
     }
     if (poisoned && id >= 0) w = NAN;
     if (lane < a.top_k) {

@@ -81,6 +81,43 @@ def test_choices_that_float32_does_not_tell_apart(score):
 
 
 @pytest.mark.parametrize("score", [qm.SCORE_SOFTMAX, qm.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,k", [(48, 6), (64, 40), (256, 8), (1024, 20)])
+def test_chains_of_choices_next_to_one_another(score, E, k):
+    # neighbours a unit or a few of float32 apart: shorter and longer than the slots, across the last slot and
+    # through every expert, up and down, on top of one another and far below the row's largest
+    near = 1 + torch.arange(E, dtype=torch.float64).mul(2.0 ** -22)
+    rows = [near, near.flip(0), -near, near.mul(-70), near.mul(0.25).where(torch.arange(E) % 3 > 0, torch.tensor(-5.0).double())]
+    logits = torch.stack(rows).float()
+    logits = torch.cat((logits, logits[:, torch.randperm(E, generator=torch.Generator().manual_seed(E))]))
+    spread = torch.randn(2, E, generator=torch.Generator().manual_seed(1))
+    spread[0, 5:5 + k - 1] = 4.0 + torch.arange(k - 1) * 2.0 ** -21   # ends before the last slot
+    spread[1, 5:5 + k + 2] = 4.0 - torch.arange(k + 2) * 2.0 ** -21   # ends behind it
+    top = torch.cat((logits, spread))
+    top[3] -= 1.0
+    top[3, E // 2] = 20.0  # scores around exp(-90): below float32's normal range
+    for bias in (None, torch.zeros(E), torch.full((E,), 3.0)):
+        b = None if bias is None else bias.cuda()
+        _check(top.cuda(), b, k, score)
+        _check(top.cuda(), b, k, score, 8, 5, 2)
+        _check(top.cuda(), b, k, score, 8, 5, 1)
+
+
+@pytest.mark.parametrize("score", [qm.SCORE_SOFTMAX, qm.SCORE_SIGMOID])
+def test_biases_far_larger_than_the_scores(score):
+    # a group's rank is the sum of a large and a small choice: its error goes with them, not with the sum
+    g = torch.Generator().manual_seed(12)
+    logits = torch.randn(50, 64, generator=g)
+    for large in (3.0, 100.0, 1e6, 1e30):
+        bias = torch.full((64,), -large)
+        bias[::8] = large
+        _check(logits.cuda(), bias.cuda(), 12, score, 8, 4, 2)
+        _check(logits.cuda(), bias.cuda(), 12, score)
+    bias[3] = INF
+    bias[4] = -INF
+    _check(logits.cuda(), bias.cuda(), 12, score, 8, 4, 2)
+
+
+@pytest.mark.parametrize("score", [qm.SCORE_SOFTMAX, qm.SCORE_SIGMOID])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_masked_experts_and_rows(score, normalize):
     g = torch.Generator(device="cuda").manual_seed(3)
