@@ -516,7 +516,7 @@ int qmoe_route_scores_backward(const float* grad_weights, const void* logits, in
  * power of two, at least 2^-126, that holds its largest magnitude within 448;
  * codes are x / scale (an exact quotient) rounded to nearest, ties to even.  A
  * zero block has the scale 2^-126; a block with a NaN or an infinity has the
- * scale NaN and codes 0.  rows*K <= 2^34.
+ * scale NaN and codes 0.
  *
  * qmoe_blocks_quantize_weights: x dtype [E, rows, K] dense, in squares of 128 x
  * 128, to codes [E, rows, K] and scales [E, ceil(rows/128), ceil(K/128)]; with
@@ -526,6 +526,10 @@ int qmoe_route_scores_backward(const float* grad_weights, const void* logits, in
  *
  * qmoe_blocks_dequantize, qmoe_blocks_dequantize_weights: the values, code * scale in
  * float32, rounded to dtype; scales may be any float32 values (a checkpoint's).
+ *
+ * K (and the rows of a matrix of weights) at most 2^20, E below 2^16, at most
+ * 2^34 values, else QMOE_ERR_UNSUPPORTED.  No rows: QMOE_OK, nothing is enqueued.
+ * Outputs are dense and must not overlap the inputs.
  */
 int qmoe_blocks_quantize(const void* x, int64_t row_stride, int64_t rows, int32_t K, int32_t dtype,
                       uint8_t* codes, float* scales, void* stream);
@@ -550,9 +554,9 @@ int qmoe_blocks_dequantize_weights(const uint8_t* codes, const float* scales, in
  * The scales may be any float32 values; the product of two is rounded to
  * float32, so it must stay in float32's range (below 2^-126 it may count as 0).
  * A NaN scale or code makes the outputs it enters NaN.  With sorted_routes
- * a_rows * K < 2^31; dtype F16 or BF16, N and K at most 2^20, K a multiple of 16, E <= 1024, rows
- * < 2^24, rows * N at most 2^40 (else QMOE_ERR_UNSUPPORTED).  rows = 0 returns
- * QMOE_OK and enqueues nothing.
+ * a_rows * K < 2^31; N and K at most 2^20, K a multiple of 16, rows < 2^24,
+ * rows * N at most 2^40 (else QMOE_ERR_UNSUPPORTED); E <= 1024.  rows = 0
+ * returns QMOE_OK and enqueues nothing.
  */
 int qmoe_blocks_matmul(const uint8_t* a_codes, const float* a_scales, int64_t a_rows,
                     const uint8_t* w_codes, const float* w_scales, int32_t E, int32_t N, int32_t K,

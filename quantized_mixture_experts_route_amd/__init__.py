@@ -799,7 +799,7 @@ def route_scores(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMAX
     logits: float16, bfloat16 or float32 [T, E], any row stride.  score: SCORE_SOFTMAX or SCORE_SIGMOID.
     bias float32 [E] is added to the scores for the choice alone.  Experts come in n_groups groups of
     neighbours, ranked by the sum of their group_top (1 or 2) best choices; the top_groups best (all, if
-    not given) take part.  Choices are compared in float64, ties go to the lower index.  normalize divides
+    not given) take part.  Choices are compared as float64 values, ties go to the lower index.  normalize divides
     a token's weights by their sum; scale multiplies them.  An expert with a logit of -inf is never
     chosen; slots without an expert left have the id -1 and the weight 0, which permute drops.  Autograd
     does not record the call: route_scores_backward is its gradient."""
@@ -814,8 +814,9 @@ def route_scores(logits: torch.Tensor, top_k: int, *, score: int = SCORE_SOFTMAX
         top_groups = n_groups
     _fit(E, top_k, score, n_groups, top_groups, group_top)
     b = None if bias is None else _tensor(bias, "bias", dev, torch.float32, (E,))
-    ids = logits.new_empty((T, max(top_k, 0)), dtype=torch.int32)
-    weights = logits.new_empty((T, max(top_k, 0)), dtype=torch.float32)
+    slots = (T, min(max(top_k, 0), E))  # the library refuses others
+    ids = logits.new_empty(slots, dtype=torch.int32)
+    weights = logits.new_empty(slots, dtype=torch.float32)
     _check(load_library().qmoe_route_scores(
         logits.data_ptr(), stride, T, E, dt, b, top_k, score, n_groups, top_groups, group_top, bool(normalize),
         scale, ids.data_ptr(), weights.data_ptr(), _current(dev)))
@@ -1051,6 +1052,7 @@ def activate(y: torch.Tensor, *, activation: int = ACT_SWIGLU, swiglu_fusion: in
             return activate(y, activation=activation, swiglu_fusion=swiglu_fusion, activation_alpha=activation_alpha,
                             activation_beta=activation_beta, swiglu_limit=swiglu_limit, out=out)
     rows, I, stride, dt = _pairs(y)
+    _fit(activation, swiglu_fusion)
     if out is None:
         out = y.new_empty((rows, I))
         to = out.data_ptr()
@@ -1074,6 +1076,7 @@ def activate_fp8(y: torch.Tensor, *, activation: int = ACT_SWIGLU, swiglu_fusion
                                 activation_alpha=activation_alpha, activation_beta=activation_beta,
                                 swiglu_limit=swiglu_limit)
     rows, I, stride, dt = _pairs(y)
+    _fit(activation, swiglu_fusion)
     codes = y.new_empty((rows, I), dtype=FP8_DTYPE)
     scales = y.new_empty((rows, _fp8_blocks(I)), dtype=torch.float32)
     _check(load_library().qmoe_activate_blocks(y.data_ptr(), stride, rows, I, dt, activation, swiglu_fusion,
@@ -1094,6 +1097,7 @@ def activate_backward(grad: torch.Tensor, y: torch.Tensor, *, activation: int = 
                                      activation_alpha=activation_alpha, activation_beta=activation_beta,
                                      swiglu_limit=swiglu_limit)
     rows, I, stride, dt = _pairs(y)
+    _fit(activation, swiglu_fusion)
     gstride = _rows(grad, "grad", dev, rows)
     if grad.dtype is not y.dtype or grad.shape[1] != I:
         raise ValueError(f"grad is {grad.dtype} {tuple(grad.shape)}, expected {y.dtype} {(rows, I)}")

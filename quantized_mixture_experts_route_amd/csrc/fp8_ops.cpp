@@ -32,6 +32,13 @@ int check_sixteens(const char* name, int32_t n)
     return QMOE_OK;
 }
 
+int check_values(int64_t rows, int32_t K)
+{
+    if (K > kMaxWidth) return set_error(QMOE_ERR_UNSUPPORTED, "K=%d must be at most 2^20", K);
+    if (rows > kMaxValues / K) return set_error(QMOE_ERR_UNSUPPORTED, "rows*K must be at most 2^34");
+    return QMOE_OK;
+}
+
 int check_scores(int64_t T, int32_t E, int32_t dtype, int32_t top_k, int32_t score, float scale)
 {
     if (T < 0) return set_error(QMOE_ERR_INVALID_ARG, "T=%lld < 0", (long long)T);
@@ -163,7 +170,7 @@ int qmoe_blocks_quantize(const void* x, int64_t row_stride, int64_t rows, int32_
     if (rows < 0 || K < 1) return set_error(QMOE_ERR_INVALID_ARG, "rows=%lld, K=%d", (long long)rows, K);
     QMOE_TRY(check_dtype(dtype));
     QMOE_TRY(check_sixteens("K", K));
-    if (rows > kMaxValues / K) return set_error(QMOE_ERR_UNSUPPORTED, "rows*K must be at most 2^34");
+    QMOE_TRY(check_values(rows, K));
     if (rows == 0) return finish(hipSuccess, "");
     QMOE_TRY(check_rows("x", x, rows, row_stride, K, elem_bytes(dtype)));
     QMOE_TRY(check_fp8("output", codes, scales));
@@ -194,7 +201,7 @@ int qmoe_blocks_dequantize(const uint8_t* codes, const float* scales, int64_t ro
     if (rows < 0 || K < 1) return set_error(QMOE_ERR_INVALID_ARG, "rows=%lld, K=%d", (long long)rows, K);
     QMOE_TRY(check_dtype(dtype));
     QMOE_TRY(check_sixteens("K", K));
-    if (rows > kMaxValues / K) return set_error(QMOE_ERR_UNSUPPORTED, "rows*K must be at most 2^34");
+    QMOE_TRY(check_values(rows, K));
     if (rows == 0) return finish(hipSuccess, "");
     QMOE_TRY(check_fp8("input", codes, scales));
     QMOE_TRY(check_rows("out", out, rows, K, K, elem_bytes(dtype)));

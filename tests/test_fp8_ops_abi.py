@@ -159,3 +159,9 @@ def test_binding_refuses_tensors_of_the_host():
             call()
     with pytest.raises(ValueError, match="top_k"):
         qm.fp8_matmul(codes, scales, codes, scales, sorted_routes=torch.zeros(4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name,defaults", [("quantize", dict(QUANT, stride=1 << 31)), ("dequantize", BACK)])
+@pytest.mark.parametrize("K", [(1 << 20) + 16, (1 << 31) - 16])  # the count of the longest row's blocks left 32 bits
+def test_conversions_refuse_wider_rows(name, defaults, K):
+    _refused("qmoe_blocks_" + name, defaults, dict(rows=1, K=K), UNSUP)
