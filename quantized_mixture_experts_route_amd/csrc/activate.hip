@@ -11,7 +11,11 @@
 // in float32, rounded once.  NaN passes through.
 //
 // Every value is read and written once, with some 20 to 40 operations for each
-// output: bound by HBM.
+// output: bound by HBM (8192 rows of 2 x 14336 bf16: 138 us, 5.1 TB/s, what a copy
+// reaches; straight to 8 bits 154, 3.8 TB/s, with codes for half of the bytes and
+// the same operations; the gradient 205, 5.7 TB/s), small calls by the launch
+// (3.2 us of the GPU).  Eight outputs a thread: 16 bytes a load and store, and 16
+// threads are a block of 128, whose maximum stays within a row of lanes.
 #include <algorithm>
 
 #include "fp8_block.h"

@@ -14,6 +14,14 @@
 // block, and the addend meet in float32.  On normal values that leaves 2e-5 of the
 // result (2-norm), a hundredth of the rounding to 16 bits; outputs in float32 would
 // need the operands as f16 at half the rate, and are refused.
+//
+// What bounds it: large products the clock under the card's power limit (8192 x
+// 28672 x 4096 over 8 experts 900 us, 2.1 PFLOP/s at about 1.8 GHz, the matrix
+// units busy in half of the cycles; the unscaled library product of the same sizes
+// 736; 14336 inputs, 4096 outputs, 8192 rows 535 us; 8192^3 470 to 500); products
+// of few rows HBM (60 rows over 512 experts, 2048 inputs, 1536 outputs: 39 us, 4.6
+// TB/s out of the cache), and the smallest the chain of table, routes, rows and sum
+// (2 rows over 8 experts: 7.7 us).
 #include "expert_tiles.h"
 #include "fp8_ops.h"
 #include "fp8_shape.h"

@@ -423,6 +423,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
     }
 }
 
+// A row is read and written once and its slots' logits once more; sums of a token by DPP.  Bound by HBM where there
+// are many tokens (65536 tokens of 256 experts, top-8, sigmoid: 40 us for 138 MB, 3.5 TB/s), else by the launch.
 template <int DT, int EPL>
 __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(RouteScoresArgs a)
 {
