@@ -76,11 +76,11 @@ constexpr int kSlots = kWave;          // scales a wavefront loads in a step
 // Bytes that a tile reads of codes or scales; its descriptor from byte `at` on.
 struct Span {
     const uint8_t* base;
-    uint32_t bytes;
+    uint32_t size;
     __device__ inline __amdgpu_buffer_rsrc_t from(uint32_t at) const
     {
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0,
-                                                 mx_bytes_left(__builtin_amdgcn_readfirstlane(bytes), at), 0x00020000);
+        const uint32_t bytes = __builtin_amdgcn_readfirstlane(size);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + at), 0, mx_bytes_left(bytes, at), 0x00020000);
     }
 };
 
