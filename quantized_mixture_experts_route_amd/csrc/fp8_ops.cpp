@@ -131,6 +131,7 @@ int qmoe_route_scores(const void* logits, int64_t row_stride, int64_t T, int32_t
     a.n_groups = n_groups;
     a.top_groups = top_groups;
     a.group_top = group_top;
+    a.group_size = E / n_groups;
     a.normalize = normalize != 0;
     a.scale = scale;
     a.ids = ids;

@@ -21,6 +21,7 @@ struct RouteScoresArgs {
     int n_groups;
     int top_groups;
     int group_top;
+    int group_size;  // E / n_groups
     int normalize;
     float scale;
     int32_t* ids;               // [T, top_k]: written forward, read backward

@@ -42,6 +42,22 @@ __device__ inline double value_of(uint64_t key)
     return __builtin_bit_cast(double, key >> 63 ? key & ~(1ull << 63) : ~key);
 }
 
+// The same for floats, -inf and all (no NaN); -0 as 0.
+__device__ inline uint32_t ordered(float c)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, c + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ inline float float_of(uint32_t key)
+{
+    return __builtin_bit_cast(float, key ^ ((int32_t)key < 0 ? 0x80000000u : ~0u));
+}
+
+// Maximum of a wavefront's floats without NaN: as integers it takes a DPP operation a step, where one of floats
+// that keeps -0 and NaN in their places takes four.
+__device__ inline float wave_largest(float v) { return float_of(wave_max_u32(ordered(v))); }
+
 __device__ inline double wave_sum_f64(double v)
 {
     auto plus = [](double x, uint64_t o) { return x + __builtin_bit_cast(double, o); };
@@ -89,43 +105,33 @@ __device__ inline int wave_best(uint64_t key)
 // Sum over the chosen slots (lanes), in a fixed order.
 __device__ inline float sum_slots(float v) { return wave_sum_f32(v); }
 
-// exp(-|l|), and the logistic function and its rest from it.
-__device__ inline float logistic_of(float l)
-{
-    const float e = expf(-fabsf(l));
-    return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
-}
-
 // A lane's chosen expert's score over the largest of the chosen (m their largest logit), from logits so
 // far below 0 too that every score is 0 to float32: sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).
 __device__ inline float relative_score(bool sigmoid, float l, float m)
 {
-    if (!sigmoid) return expf(l - m);
-    return expf(fminf(l, 0.0f) - fminf(m, 0.0f)) * ((1.0f + expf(-fabsf(m))) / (1.0f + expf(-fabsf(l))));
+    if (!sigmoid) return exp_of(l - m);
+    return exp_of(fminf(l, 0.0f) - fminf(m, 0.0f)) * ((1.0f + exp_minus(fabsf(m))) / (1.0f + exp_minus(fabsf(l))));
 }
 
 // ---------------------------------------------------------------- the choice
 // One wavefront a token, EPL neighbouring experts a lane: EPL * lane + j, so that the lowest lane of several
 // holds the lowest index.  Both forms leave slot s's expert in lane s (-1: none is left).
 
-// Choices in float32, and float64 where they come too near one another: two choices differ in float64 as they do
-// in float32 if they are further apart than kNear (1 + |choice|), or than kNear of it where there is no bias.  A
-// score in float32 is off by 8 units of 2^-24 (sigmoid) or 30 (softmax: the sum's rounding and that of l - m, whose
-// mean over the scores is below log E), a sum with a bias by one more; kNear is 64 units for the difference of two.
-// Choices in a chain of near ones, which may reach past the last slot, are put in order by their float64 values,
-// one a lane.  False where that does not do: groups that near one another at the last place, near choices by
-// softmax with a bias (their sum over all experts counts), groups of other sizes.
+// Choices in float32, and float64 where they come too near one another.  A word holds a choice's bits in their
+// order, the last log2(EPL) of them replaced by the expert's place in its lane, so that a lane sorts its words by
+// minima and maxima alone.  In units u of 2^-24: a score in float32 is off by 8 u of it (sigmoid) or 30 u of 1
+// (softmax: the sum's rounding, and that of l - m, which keeps the order and whose mean over the scores is below
+// log E), its sum with a bias by one u of that, and the place by up to 30 u, downwards.  So two choices differ in
+// float64 as they do here if they are further apart than 60 u + 32 u (|c| + |d|), without a bias 46 u |c|; kNear
+// is 64 u.  Choices in a chain of near ones, which may reach past the last slot, are put in order by their float64
+// values, one a lane, equal ones by their index.  False where that does not do: groups that near one another at
+// the last place, near choices by softmax with a bias (their sum over all experts counts), groups of other sizes.
 constexpr float kNear = 0x1p-18f;
 
-__device__ inline uint32_t key32(float c)
-{
-    const uint32_t b = __builtin_bit_cast(uint32_t, c + 0.0f);
-    return c == -INFINITY ? 0u : (int32_t)b < 0 ? ~b : b | 0x80000000u;
-}
-
+template <int EPL>
 __device__ inline float value32(uint32_t key)
 {
-    return __builtin_bit_cast(float, (int32_t)key < 0 ? key & 0x7fffffffu : ~key);
+    return float_of(key & ~(uint32_t)(EPL - 1));
 }
 
 struct Two32 {
@@ -143,6 +149,29 @@ __device__ inline Two32 merge_dpp(Two32 a)
     return merge(a, Two32{dpp_u32<CTRL>(a.first), dpp_u32<CTRL>(a.second)});
 }
 
+// Largest first: Batcher's odd-even merge sort.
+template <int N>
+__device__ inline void sort_down(uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2) {
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k) {
+#pragma unroll
+                for (int i = 0; i < k; ++i) {
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t hi = max(v[i + j], v[i + j + k]);
+                        v[i + j + k] = min(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Whether a group is a whole power of two of lanes.
 __device__ inline bool groups_fit(int size, int epl)
 {
@@ -150,26 +179,26 @@ __device__ inline bool groups_fit(int size, int epl)
     return size % epl == 0 && (lanes & (lanes - 1)) == 0;
 }
 
-template <int EPL>
-__device__ inline bool choose_fast(const RouteScoresArgs& a, int lane, const float (&score)[EPL], const float (&bias)[EPL],
-                                   const float (&l)[EPL], float m, int& id)
+template <int DT, int EPL>
+__device__ inline bool choose_fast(const RouteScoresArgs& a, const typename RowType<DT>::Raw* row, int lane,
+                                   const float (&score)[EPL], const float (&bias)[EPL], const float (&l)[EPL], float m,
+                                   int& id)
 {
-    uint32_t key[EPL];
+    uint32_t key[EPL];  // masked: 0, which no other word is
     const float base = a.bias ? 1.0f : 0.0f;
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const float c = score[j] + bias[j];
-        nan |= c != c;
-        key[j] = l[j] == -INFINITY ? 0u : key32(c);
+        nan |= c != c && l[j] != -INFINITY;
+        key[j] = l[j] == -INFINITY || c == -INFINITY ? 0u : (ordered(c) & ~(uint32_t)(EPL - 1)) | j;
     }
     if (__any(nan)) return false;
+    sort_down(key);
     if (a.top_groups < a.n_groups) {
-        const int size = a.E / a.n_groups, lanes = size / EPL;
-        if (!groups_fit(size, EPL)) return false;
-        Two32 best{key[0], 0};
-#pragma unroll
-        for (int j = 1; j < EPL; ++j) best = merge(best, Two32{key[j], 0});
+        const int lanes = a.group_size / EPL;
+        if (!groups_fit(a.group_size, EPL)) return false;
+        Two32 best{key[0], EPL > 1 ? key[EPL > 1] : 0};
         if (lanes > 1) best = merge_dpp<kDppXor1>(best);
         if (lanes > 2) best = merge_dpp<kDppXor2>(best);
         if (lanes > 4) best = merge_dpp<kDppHalfMirror>(best);
@@ -177,74 +206,61 @@ __device__ inline bool choose_fast(const RouteScoresArgs& a, int lane, const flo
         for (int d = 16; d < lanes; d <<= 1) {
             best = merge(best, Two32{(uint32_t)__shfl_xor((int)best.first, d, kWave), (uint32_t)__shfl_xor((int)best.second, d, kWave)});
         }
-        float rank = best.first ? value32(best.first) : -INFINITY, size_of = best.first ? fabsf(rank) : 0.0f;
+        float rank = best.first ? value32<EPL>(best.first) : -INFINITY, size_of = best.first ? fabsf(rank) : 0.0f;
         if (a.group_top == 2 && best.second) {
-            rank += value32(best.second);
-            size_of += fabsf(value32(best.second));
+            const float second = value32<EPL>(best.second);
+            rank += second;
+            size_of += fabsf(second);
         }
         const int mine = lane / lanes;
-        int before = 0;  // groups ahead of the lane's
-        for (int g = 0; g < a.n_groups; ++g) {
-            const float other = readlane_f32(rank, g * lanes);
-            before += other > rank || (other == rank && g < mine);
-        }
+        int before = 0;  // groups ahead of the lane's; equal ones are kept or dropped together
+        for (int g = 0; g < a.n_groups; ++g) before += readlane_f32(rank, g * lanes) > rank;
         const bool in = mine < a.n_groups, kept = before < a.top_groups;
-        const float least = -wave_max_f32(in && kept ? -rank : -INFINITY), most = wave_max_f32(in && !kept ? rank : -INFINITY);
-        // a rank's error goes with what it is the sum of, which with a bias may be far larger than the rank;
-        // without an expert left in the best of the others nothing hangs on it (least - most is inf or NaN)
-        const float scale = a.bias ? 1.0f + wave_max_f32(size_of) : least;
-        if (least - most <= 4.0f * kNear * scale + 0x1p-120f) return false;
+        const float least = -wave_largest(in && kept ? -rank : -INFINITY), most = wave_largest(in && !kept ? rank : -INFINITY);
+        // A rank's error goes with what it is the sum of, which with a bias may be far larger than the rank; without
+        // one, a score's relative error also has the rounding of l - m, up to 64 u.  Without an expert left in the
+        // best of the others nothing hangs on it.
+        const float scale = a.bias ? 2.0f + wave_largest(size_of) : 4.0f * least;
+        if (__popcll(__ballot(in && kept && rank > -INFINITY)) > a.top_groups * lanes) return false;
+        if (most > -INFINITY && !(least - most > kNear * scale + 0x1p-120f)) return false;
         if (!kept) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) key[j] = 0;
         }
     }
-    float last = INFINITY, logit = -INFINITY;
-    bool in_doubt = false;
+    auto near = [&](float before, float c) { return !(before - c > kNear * (base + fabsf(c))); };  // inf and inf too
+    uint32_t own = 0, last = 0;
     int n = 0;  // candidates, in lanes 0 .. n - 1
     for (;; ++n) {
-        uint32_t top = key[0];
-#pragma unroll
-        for (int j = 1; j < EPL; ++j) top = max(top, key[j]);
-        const uint32_t mine = top;
-        top = wave_max_u32(top);
+        const uint32_t top = wave_max_u32(key[0]);
         if (top == 0) break;
-        const float c = value32(top);
-        const bool near = last - c <= kNear * (base + fabsf(c));
-        if (n >= a.top_k && !near) break;
-        if (n == kWave) return false;
-        in_doubt |= near;
-        last = c;
-        const int from = __builtin_ctzll(__ballot(mine == top));
-        int here = EPL - 1;
-        float value = l[EPL - 1];
-#pragma unroll
-        for (int j = EPL - 2; j >= 0; --j) {
-            here = key[j] == top ? j : here;
-            value = key[j] == top ? l[j] : value;
+        if (n >= a.top_k) {
+            if (!near(value32<EPL>(last), value32<EPL>(top))) break;
+            if (n == kWave) return false;
         }
-        const int e = from * EPL + __builtin_amdgcn_readlane(here, from);
-        value = readlane_f32(value, from);
+        last = top;
+        const int from = __builtin_ctzll(__ballot(key[0] == top));
         if (lane == n) {
-            id = e;
-            logit = value;
+            own = top;
+            id = from * EPL + (int)(top & (EPL - 1));
         }
+        const bool taken = lane == from;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            if (lane * EPL + j == e) key[j] = 0;
-        }
+        for (int j = 0; j < EPL; ++j) key[j] = taken ? (j + 1 < EPL ? key[j + 1 < EPL ? j + 1 : j] : 0u) : key[j];
     }
-    if (in_doubt) {
+    const uint32_t before = (uint32_t)__shfl_up((int)own, 1, kWave);
+    if (__any(lane > 0 && lane < n && near(value32<EPL>(before), value32<EPL>(own)))) {
         if (!a.sigmoid && a.bias) return false;
+        const double logit = id < 0 ? 0.0 : (double)RowType<DT>::value(row[id]);
         // softmax without a bias: exp(l - m) orders as the scores do
-        const double score64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)logit)) : exp((double)logit - (double)m);
+        const double score64 = a.sigmoid ? 1.0 / (1.0 + exp(-logit)) : exp(logit - (double)m);
         const uint64_t exact = id < 0 ? 0 : key_of(score64 + (a.bias ? (double)a.bias[id] : 0.0));
-        int before = 0;
+        int ahead = 0;
         for (int i = 0; i < n; ++i) {
             const uint64_t other = readlane_u64(exact, i);
-            before += other > exact || (other == exact && __builtin_amdgcn_readlane(id, i) < id);
+            ahead += other > exact || (other == exact && __builtin_amdgcn_readlane(id, i) < id);
         }
-        id = __builtin_amdgcn_ds_permute((lane < n ? before : lane) * 4, id);
+        id = __builtin_amdgcn_ds_permute((lane < n ? ahead : lane) * 4, id);
     }
     if (lane >= a.top_k) id = -1;
     return true;
@@ -276,7 +292,7 @@ __device__ inline int choose_exactly(const RouteScoresArgs& a, int lane, const f
     for (int j = 0; j < EPL; ++j) key[j] = l[j] == -INFINITY ? 0 : key_of(score[j] + (double)bias[j]);
 
     if (a.top_groups < a.n_groups) {
-        const int size = a.E / a.n_groups, lanes = size / EPL;
+        const int size = a.group_size, lanes = size / EPL;
         if (groups_fit(size, EPL)) {
             Two best{key[0], 0};
 #pragma unroll
@@ -345,8 +361,9 @@ __device__ inline int choose_exactly(const RouteScoresArgs& a, int lane, const f
 }
 
 // What bounds it: few tokens, the launch and the chain of wavefront maxima, one for each slot; many, the
-// instructions of a token, about 800 (65536 tokens, 256 experts in 8 groups, top-8: 84 us for 72 MB; with every
-// choice in float64 102; 4096 tokens of 1024 experts, top-16: 24 us against 33).  A lane holds neighbouring experts
+// instructions of a token, about 650 (65536 tokens, 256 experts in 8 groups, top-8: 71 us for 72 MB; with every
+// choice in float64 102; 4096 tokens of 1024 experts, top-16: 17 us against 33; without the sort within a lane
+// 84 and 24; tokens in turn in a launch of 2048 workgroups: 90).  A lane holds neighbouring experts
 // so that a group is a few lanes and its best two come by DPP; a wavefront a token, since a token's maxima are
 // then one reduction each and nothing waits at a barrier.
 template <int DT, int EPL>
@@ -389,7 +406,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
             m = fmaxf(m, l[j]);
             nan |= l[j] != l[j];
         }
-        m = wave_max_f32(m);
+        m = wave_largest(m);
         poisoned = __any(nan) || m == INFINITY;
         float part = 0.0f;
 #pragma unroll
@@ -398,23 +415,24 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_kernel(RouteScoresAr
             part += score[j];
         }
         sum = wave_sum_f32(part);
-        const float inverse = 1.0f / sum;
+        float inverse = __builtin_amdgcn_rcpf(sum);  // of a sum within [1, 1024]
+        inverse = fmaf(fmaf(-sum, inverse, 1.0f), inverse, inverse);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) score[j] *= inverse;
     }
     int id = -1;
-    if (poisoned || !choose_fast<EPL>(a, lane, score, bias, l, m, id)) {
+    if (poisoned || !choose_fast<DT, EPL>(a, row, lane, score, bias, l, m, id)) {
         id = choose_exactly<EPL>(a, lane, l, bias, m, poisoned, choices[wave]);
     }
     const float chosen = id >= 0 ? RowType<DT>::value(row[id]) : -INFINITY;
     float w = 0.0f;
     if (a.normalize) {
-        const float top = wave_max_f32(chosen);  // NaN compares false and is skipped
+        const float top = wave_largest(chosen == chosen ? chosen : -INFINITY);
         const float r = id < 0 ? 0.0f : relative_score(a.sigmoid, chosen, top);
         const float total = sum_slots(r);
         if (id >= 0) w = r / total;
     } else if (id >= 0) {
-        w = a.sigmoid ? logistic_of(chosen) : expf(chosen - m) / sum;
+        w = a.sigmoid ? logistic(chosen).s : exp_of(chosen - m) / sum;
     }
     if (poisoned && id >= 0) w = NAN;
     if (lane < a.top_k) {
@@ -453,14 +471,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     float mean = 0.0f;      // softmax: sum G s
     float m = -INFINITY, total = 1.0f;
     if (a.normalize) {
-        const float top = wave_max_f32(chosen);
+        const float top = wave_largest(chosen == chosen ? chosen : -INFINITY);
         const float r = id < 0 ? 0.0f : relative_score(a.sigmoid, chosen, top);
         const float sum = sum_slots(r);
         const float w = id < 0 ? 0.0f : r / sum;
         const float centre = sum_slots(id < 0 ? 0.0f : g * w);
-        to_slot = id < 0 ? 0.0f : w * (g - centre) * (a.sigmoid ? logistic_of(-chosen) : 1.0f);
+        to_slot = id < 0 ? 0.0f : w * (g - centre) * (a.sigmoid ? logistic(chosen).rest : 1.0f);
     } else if (a.sigmoid) {
-        to_slot = id < 0 ? 0.0f : g * (logistic_of(chosen) * logistic_of(-chosen));
+        const Logistic s = logistic(chosen);
+        to_slot = id < 0 ? 0.0f : g * (s.s * s.rest);
     } else {
         bool nan = false;
 #pragma unroll
@@ -468,12 +487,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
             m = fmaxf(m, l[j]);
             nan |= l[j] != l[j];
         }
-        m = __any(nan) ? NAN : wave_max_f32(m);
+        m = __any(nan) ? NAN : wave_largest(m);
         float part = 0.0f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) part += l[j] == -INFINITY ? 0.0f : expf(l[j] - m);
+        for (int j = 0; j < EPL; ++j) part += l[j] == -INFINITY ? 0.0f : exp_of(l[j] - m);
         total = wave_sum_f32(part);
-        mean = sum_slots(id < 0 ? 0.0f : g * (expf(chosen - m) / total));
+        mean = sum_slots(id < 0 ? 0.0f : g * (exp_of(chosen - m) / total));
     }
     float out[EPL] = {};
     for (int s = 0; s < a.top_k; ++s) {
@@ -488,7 +507,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_scores_backward_kernel(Rout
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + kWave * j;
         if (e >= a.E) continue;
-        if (!a.sigmoid && !a.normalize) out[j] = l[j] == -INFINITY ? 0.0f : expf(l[j] - m) / total * (out[j] - mean);
+        if (!a.sigmoid && !a.normalize) out[j] = l[j] == -INFINITY ? 0.0f : exp_of(l[j] - m) / total * (out[j] - mean);
         ((Raw*)a.grad_logits)[t * a.E + e] = RowType<DT>::round(out[j]);
     }
 }
