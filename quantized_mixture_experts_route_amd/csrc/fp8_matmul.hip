@@ -439,26 +439,28 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 16 rows against 32 weight rows; the eight wavefronts share K block by block, operands straight from
-// memory, every load of four blocks a wavefront under way at once.  Their sums meet in LDS, in the order of the
-// wavefronts.  For products of few tiles, which are a chain of latencies: the tiled kernel walks K step by step.
-constexpr int kRowsWaves = 8, kRowsTile = 16, kRowsColumns = 32, kRowsAhead = 4;
+// Up to 16 rows against COLUMNS (16 or 32) weight rows; the eight wavefronts share K block by block, operands
+// straight from memory, every load of four blocks a wavefront under way at once (a ring that loads a block's place
+// again behind its products was slower: one row, 14336 inputs, 20.4 us against 18.7).  Their sums meet in LDS, in
+// the order of the wavefronts.  For products of few tiles, which are a chain of latencies: the tiled kernel walks K
+// step by step.
+constexpr int kRowsWaves = 8, kRowsTile = 16, kRowsAhead = 4;
 
-template <int DT>
+template <int DT, int COLUMNS>
 __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
 {
-    constexpr int THREADS = 64 * kRowsWaves, PITCH = kRowsColumns + 4;
+    constexpr int THREADS = 64 * kRowsWaves, NT = COLUMNS / 16, PITCH = COLUMNS + 4;
     __shared__ int first[kMaxExperts + 1], scratch[kMaxExperts + 1];
     __shared__ __align__(16) float sums[kRowsWaves][kRowsTile][PITCH];
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int K = a.K, blocks = (K + kFp8Block - 1) / kFp8Block, n_blocks = (a.N + kFp8Block - 1) / kFp8Block;
     build_tile_list<kRowsTile, THREADS>(first, scratch, a.offsets, a.E, a.rows);
-    const int n_tiles = (a.N + kRowsColumns - 1) / kRowsColumns;
+    const int n_tiles = (a.N + COLUMNS - 1) / COLUMNS;
     const int total = __builtin_amdgcn_readfirstlane(mx_items(first[a.E], n_tiles, a.rows, kRowsTile, a.E));
     clear_behind<THREADS>(a, scratch[a.E]);
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const TileItem t = item_at<kRowsTile, kRowsColumns>(
+        const TileItem t = item_at<kRowsTile, COLUMNS>(
             first, [&](int e) { return __builtin_amdgcn_readfirstlane(scratch[e]); }, a.E, n_tiles, item, total);
         int source = min(c, t.n - 1);  // from the tile's first row where there are no routes
         if (a.sorted_routes) {
@@ -467,15 +469,15 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
         }
         const int64_t a0 = a.sorted_routes ? 0 : t.row0, a_rows = a.sorted_routes ? a.a_rows : t.n;
         const int64_t w0 = (int64_t)t.expert * a.N + t.n0;
-        const int w_rows = min(kRowsColumns, a.N - t.n0);
+        const int w_rows = min(COLUMNS, a.N - t.n0);
         const Span x_span{a.a_codes + a0 * K, (uint32_t)(a_rows * K)}, w_span{a.w_codes + w0 * K, (uint32_t)(w_rows * K)};
         const Span sx_span{(const uint8_t*)(a.a_scales + a0 * blocks), (uint32_t)(a_rows * blocks * 4)};
         const float* const sw_row = a.w_scales + ((int64_t)t.expert * n_blocks + t.n0 / kFp8Block) * blocks;
         const uint32_t x_at = source < 0 ? kMxOutside : source * (uint32_t)K, sx_at = source < 0 ? kMxOutside : source * (uint32_t)blocks * 4;
         const uint32_t w_at = c * (uint32_t)K;  // rows behind N: out of bounds
-        f32x4 acc[2] = {};
+        f32x4 acc[NT] = {};
         for (int b0 = wave; b0 < blocks; b0 += kRowsWaves * kRowsAhead) {
-            u32x4 x[kRowsAhead][2], w[kRowsAhead][2][2];
+            u32x4 x[kRowsAhead][2], w[kRowsAhead][NT][2];
             float sx[kRowsAhead], sw[kRowsAhead];
 #pragma unroll
             for (int q = 0; q < kRowsAhead; ++q) {
@@ -489,7 +491,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
                     const bool in = there && at + k < (uint32_t)K;
                     x[q][h] = __builtin_amdgcn_raw_buffer_load_b128(xr, in && source >= 0 ? x_at + k : kMxOutside, 0, 0);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < NT; ++n) {
                         w[q][n][h] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? w_at + (uint32_t)(n * 16) * K + k : kMxOutside, 0, 0);
                     }
                 }
@@ -500,7 +502,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
             for (int q = 0; q < kRowsAhead; ++q) {
                 const float f = sx[q] * sw[q];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < NT; ++n) {
                     const f32x4 p = block_product(operand(w[q][n][0], w[q][n][1]), operand(x[q][0], x[q][1]));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f, p[i], acc[n][i]);
@@ -508,13 +510,13 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
             }
         }
 #pragma unroll
-        for (int n = 0; n < 2; ++n) *reinterpret_cast<f32x4*>(&sums[wave][c][n * 16 + g * 4]) = acc[n];
+        for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(&sums[wave][c][n * 16 + g * 4]) = acc[n];
         __syncthreads();
-        const int row = threadIdx.x / kRowsColumns, column = threadIdx.x % kRowsColumns;
-        float sum = 0.0f;
+        const int row = threadIdx.x / COLUMNS, column = threadIdx.x % COLUMNS;
+        if (row < t.n && t.n0 + column < a.N) {  // t.n <= kRowsTile
+            float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kRowsWaves; ++i) sum += sums[i][row][column];
-        if (row < t.n && t.n0 + column < a.N) {
+            for (int i = 0; i < kRowsWaves; ++i) sum += sums[i][row][column];
             ((uint16_t*)a.out)[(int64_t)(t.row0 + row) * a.N + t.n0 + column] = Dt<DT>::from_float(sum);
         }
         __syncthreads();
@@ -528,11 +530,11 @@ int64_t most_items(const Fp8MatmulArgs& a, int bm, int bn)
     return (experts + (a.rows - experts) / bm) * ((a.N + bn - 1) / bn);
 }
 
-template <int DT>
+template <int DT, int COLUMNS>
 hipError_t launch_rows(const Fp8MatmulArgs& a, hipStream_t s)
 {
-    const int64_t items = most_items(a, kRowsTile, kRowsColumns);
-    launch(rows_kernel<DT>, dim3((unsigned)(items < 2 * kMxCUs ? items : 2 * kMxCUs)), dim3(64 * kRowsWaves), s, a);
+    const int64_t items = most_items(a, kRowsTile, COLUMNS);
+    launch(rows_kernel<DT, COLUMNS>, dim3((unsigned)(items < 2 * kMxCUs ? items : 2 * kMxCUs)), dim3(64 * kRowsWaves), s, a);
     return hipGetLastError();
 }
 
@@ -553,7 +555,8 @@ template <int DT>
 hipError_t launch_by_shape(const Fp8MatmulArgs& a, hipStream_t s)
 {
     switch (fp8_tile(a.E, a.N, a.rows)) {
-    case Fp8Tile::kRows: return launch_rows<DT>(a, s);
+    case Fp8Tile::kRows16: return launch_rows<DT, 16>(a, s);
+    case Fp8Tile::kRows32: return launch_rows<DT, 32>(a, s);
     case Fp8Tile::k32x64s4: return launch_tiled<DT, 2, 2, 1, 2, 4>(a, 2, s);
     case Fp8Tile::k64x128s3: return launch_tiled<DT, 2, 4, 2, 2, 3>(a, 2, s);
     case Fp8Tile::k128x128s2: return launch_tiled<DT, 4, 4, 2, 2, 2>(a, 2, s);

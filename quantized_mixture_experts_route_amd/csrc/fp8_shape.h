@@ -7,8 +7,9 @@
 
 namespace qmoe {
 
-// Tile rows x columns and LDS stages; kRows: 16 x 32 with K shared by the wavefronts.
-enum class Fp8Tile { kRows, k32x64s4, k64x128s3, k128x128s2, k256x256s2 };
+// Tile rows x columns and LDS stages; kRows16 and kRows32: 16 x 16 and 16 x 32 with K shared by the
+// wavefronts.
+enum class Fp8Tile { kRows16, kRows32, k32x64s4, k64x128s3, k128x128s2, k256x256s2 };
 
 // By the tiles that an even spread of the rows over the experts makes (the host knows the offsets' sizes
 // only) for 256 CUs, and in the end by the rounds that they take.  Measured in us, inputs out of cache, the
@@ -33,6 +34,8 @@ enum class Fp8Tile { kRows, k32x64s4, k64x128s3, k128x128s2, k256x256s2 };
 //   E 128, N 2048, K 768, rows 512  -      47.7    42.1     46.2      50.1
 //                         rows 4096 -      63.7    46.2     49.3      53.5
 //   E 512, N 1536, K 2048, rows 60  61.3   39.3    36.8     44.2      49.4
+// The rows are of kRows32; where its tiles leave half of the CUs without one, kRows16 takes 13.5 us for 18.8 (E 1, N
+// 4096, K 14336, one row) and 20.1 for 26.3 (16 rows), and the same at K 2048.
 // A round of 256 x 256 (one a CU) takes about 1.6 times as long as one of 128 x 128 (two a CU), for twice
 // the work.
 inline Fp8Tile fp8_tile(int E, int N, int rows)
@@ -43,7 +46,8 @@ inline Fp8Tile fp8_tile(int E, int N, int rows)
         const int64_t m = experts == 1 ? (rows + bm - 1) / bm : mean < bm ? experts : rows / bm + (experts + 1) / 2;
         return m * ((N + bn - 1) / bn);
     };
-    if (tiles(16, 32) <= kMxCUs) return Fp8Tile::kRows;
+    if (tiles(16, 32) <= kMxCUs / 2) return Fp8Tile::kRows16;
+    if (tiles(16, 32) <= kMxCUs) return Fp8Tile::kRows32;
     if (tiles(64, 128) <= kMxCUs / 2) return Fp8Tile::k32x64s4;
     if (mean <= 32 || tiles(64, 128) <= kMxCUs) return Fp8Tile::k64x128s3;
     const int64_t middle_rounds = (tiles(128, 128) + 2 * kMxCUs - 1) / (2 * kMxCUs);

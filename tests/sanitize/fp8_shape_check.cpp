@@ -7,7 +7,7 @@
 
 int main()
 {
-    const char* const names[] = {"rows", "32x64", "64x128", "128x128", "256x256"};
+    const char* const names[] = {"rows", "rows32", "32x64", "64x128", "128x128", "256x256"};
     int E, N, rows;
     while (std::scanf("%d %d %d", &E, &N, &rows) == 3) std::puts(names[(int)qmoe::fp8_tile(E, N, rows)]);
     return 0;

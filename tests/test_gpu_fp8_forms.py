@@ -16,6 +16,9 @@ FORMS = [
     ("rows", 1, 70, [1]),
     ("rows", 4, 500, [3, 0, 17, 16, 5]),
     ("rows", 8, 33, [0, 0, 0, 0, 0, 0, 0, 2]),
+    ("rows32", 1, 4100, [3]),
+    ("rows32", 9, 800, [1, 0, 2, 9, 3, 1, 0, 0, 5, 4]),
+    ("rows32", 2, 2050, [17, 30]),
     ("32x64", 1, 2049, [130]),
     ("32x64", 3, 1000, [33, 0, 95]),
     ("32x64", 40, 200, [1] * 30 + [0] * 9 + [7, 4]),
