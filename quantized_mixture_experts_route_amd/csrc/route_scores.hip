@@ -125,7 +125,8 @@ __device__ inline float relative_score(bool sigmoid, float l, float m)
 // float64 as they do here if they are further apart than 60 u + 32 u (|c| + |d|), without a bias 46 u |c|; kNear
 // is 64 u.  Choices in a chain of near ones, which may reach past the last slot, are put in order by their float64
 // values, one a lane, equal ones by their index.  False where that does not do: groups that near one another at
-// the last place, near choices by softmax with a bias (their sum over all experts counts), groups of other sizes.
+// the last place or whose ranks leave float32's range, near choices by softmax with a bias (their sum over all
+// experts counts), groups of other sizes.
 constexpr float kNear = 0x1p-18f;
 
 template <int EPL>
@@ -212,6 +213,8 @@ __device__ inline bool choose_fast(const RouteScoresArgs& a, const typename RowT
             rank += second;
             size_of += fabsf(second);
         }
+        // two finite choices may add up to less than float32 holds, where -inf stands for a group without experts
+        if (__any(best.first && rank == -INFINITY)) return false;
         const int mine = lane / lanes;
         int before = 0;  // groups ahead of the lane's; equal ones are kept or dropped together
         for (int g = 0; g < a.n_groups; ++g) before += readlane_f32(rank, g * lanes) > rank;

@@ -118,6 +118,24 @@ def test_biases_far_larger_than_the_scores(score):
 
 
 @pytest.mark.parametrize("score", [qm.SCORE_SOFTMAX, qm.SCORE_SIGMOID])
+def test_ranks_that_leave_the_range_of_float32(score):
+    # two finite choices that add up to more, or less, than float32 holds; -inf is a group without experts
+    low = torch.finfo(F32).min
+    g = torch.Generator().manual_seed(8)
+    bias = torch.tensor([0.0] * 4 + [-1.8e38, -1.8e38, -3.3e38, -3.3e38] + [-2e38] * 4)
+    _check(torch.randn(9, 12, generator=g).cuda(), bias.cuda(), 8, score, 3, 2, 2)
+    for E, groups, kept, k in ((64, 8, 5, 24), (256, 8, 4, 60), (160, 8, 4, 30), (1024, 64, 20, 64), (48, 8, 3, 16)):
+        size, logits = E // groups, torch.randn(12, E, generator=g)
+        logits[3, :size] = logits[4, size:] = -INF
+        for named in ([0.0, low], [0.0, low, -3e38, -2e38, -1.8e38], [1.8e38, 2e38, -low, low, 0.0], [low]):
+            by_group = torch.tensor(named)[torch.randint(0, len(named), (groups, 1), generator=g)]
+            by_expert = torch.tensor(named)[torch.randint(0, len(named), (E,), generator=g)]
+            for bias in (by_group.expand(groups, size).reshape(E), by_expert):
+                for best in (1, 2):
+                    _check(logits.cuda(), bias.cuda(), k, score, groups, kept, best)
+
+
+@pytest.mark.parametrize("score", [qm.SCORE_SOFTMAX, qm.SCORE_SIGMOID])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_masked_experts_and_rows(score, normalize):
     g = torch.Generator(device="cuda").manual_seed(3)
