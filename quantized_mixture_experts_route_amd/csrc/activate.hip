@@ -85,7 +85,10 @@ __device__ inline Pair gradient(float d, float g, float u, const ActivateArgs& a
     const auto t = gate_of<GEGLU>(g, a);
     Pair r;
     r.up = d * (t.g * t.s);
-    r.gate = d * linear_of<GEGLU>(u, a) * (t.s * fmaf(t.slope, t.rest, 1.0f));
+    const float lin = linear_of<GEGLU>(u, a), slope = t.s * fmaf(t.slope, t.rest, 1.0f);
+    // d lin may leave float32's range where the slope, at most 1.13 and often next to 0, brings it back
+    const float to = d * lin;
+    r.gate = fabsf(to) == INFINITY ? d * slope * lin : to * slope;
     if constexpr (!GEGLU) {
         if (u > a.limit || u < -a.limit) r.up = 0.0f;
         if (g > a.limit) r.gate = 0.0f;

@@ -109,6 +109,26 @@ def test_nan_and_infinities(act):
     assert gy.isfinite().all() and gy[0, 0] == 1 and gy[0, 2] == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", [INTER, HALVES])
+@pytest.mark.parametrize("act", [qm.ACT_SWIGLU, qm.ACT_GEGLU])
+def test_gradients_whose_factors_leave_the_range_of_float32(act, layout, dtype):
+    # the gradient times the linear part is more than float32 holds, and the gate's slope brings it back
+    g = torch.Generator().manual_seed(9)
+    low, high = (-80.0, -30.0) if act == qm.ACT_SWIGLU else (-9.0, -6.5)
+    gate = torch.rand(24, 40, generator=g) * (high - low) + low
+    gate[0, :8] = -200.0  # a slope of 0
+    gate[1, :8] = -1e30
+    sign = torch.randint(0, 2, (2, 24, 40), generator=g) * 2 - 1
+    up = torch.exp2(60 + 10 * torch.rand(24, 40, generator=g)) * sign[0]
+    grad = (torch.exp2(68 + 10 * torch.rand(24, 40, generator=g)) * sign[1]).to(dtype)
+    y = torch.cat((gate, up), 1) if layout == HALVES else torch.stack((gate, up), 2).flatten(1)
+    _, gy = _check(y.to(dtype).cuda(), grad.cuda(), act, layout)
+    assert gy.isfinite().all() and not _split(gy, layout)[0][:2, :8].any()
+    gy = qm.activate_backward(torch.full_like(grad, INF).cuda(), y.to(dtype).cuda(), activation=act, swiglu_fusion=layout)
+    assert not np.isfinite(_split(gy, layout)[0]).any()  # what is not finite stays so
+
+
 @pytest.mark.parametrize("act", [qm.ACT_SWIGLU, qm.ACT_GEGLU])
 def test_gradient_against_differences(act):
     g = torch.Generator().manual_seed(4)
