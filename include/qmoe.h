@@ -544,10 +544,13 @@ int qmoe_blocks_dequantize_weights(const uint8_t* codes, const float* scales, in
  * Grouped product of such rows with such expert weights, one launch:
  *   out[r, n] = sum over blocks b of sa[src(r), b] * sw[e(r), n/128, b] *
  *               sum over k in b of a[src(r), k] * w[e(r), n, k]
- * dtype is F16 or BF16.  The matrix instruction adds each eight neighbouring
- * products to 2^-13 of their largest, and those sums in float32; on values as
- * tokens and weights have them the result is good to 2^-15 or better, which is
+ * dtype is F16 or BF16.  Of each eight neighbouring products the matrix
+ * instruction cuts off what lies below 2^-13 of the largest; their sums are added
+ * in float32.  On rows and weights with values around 0 the result is good to
+ * 2^-14 in the 2-norm before its rounding (measured: normal rows 1.5e-5, gated
+ * activations 3.5e-5, rows with outliers of 30 times the rest 5.6e-5), which is
  * below the rounding to 16 bits but not float32's precision: F32 is refused.
+ * Where large neighbouring products cancel, small ones beside them may be lost.
  *   a_codes, a_scales  [a_rows, K], float32 [a_rows, ceil(K/128)]
  *   w_codes, w_scales  [E, N, K], float32 [E, ceil(N/128), ceil(K/128)]
  *   expert_offsets, sorted_routes, top_k, rows, out   as in qmoe_mx_matmul

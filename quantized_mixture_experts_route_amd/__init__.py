@@ -981,7 +981,8 @@ def fp8_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
                top_k: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Grouped product of e4m3 rows with e4m3 expert weights, a float32 scale for each block of 128: out
-    [rows, N] in dtype (float16 or bfloat16; the matrix units' sums of 8-bit products are good to 2^-15).
+    [rows, N] in dtype (float16 or bfloat16; the matrix units' sums of 8-bit products are good to 2^-14 in
+    the 2-norm).
 
     a: codes [A, K], scales [A, K/128 rounded up] (fp8_quantize); w: codes [E, N, K] (or [N, K], one
     expert), scales [E, N/128, K/128 rounded up] (fp8_quantize_weights, or a checkpoint's: any float32
