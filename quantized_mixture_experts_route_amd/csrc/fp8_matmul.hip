@@ -17,13 +17,20 @@
 // about a quarter and less of f16's (2.1e-4).  Outputs in float32 would need the operands
 // as f16 at half the rate, and are refused.
 //
-// What bounds it: large products the clock under the card's power limit (8192 x
-// 28672 x 4096 over 8 experts 900 us, 2.1 PFLOP/s at about 1.8 GHz, the matrix
-// units busy in half of the cycles; the unscaled library product of the same sizes
-// 736; 14336 inputs, 4096 outputs, 8192 rows 535 us; 8192^3 470 to 500); products
-// of few rows HBM (60 rows over 512 experts, 2048 inputs, 1536 outputs: 39 us, 4.6
-// TB/s out of the cache), and the smallest the chain of table, routes, rows and sum
-// (2 rows over 8 experts: 7.7 us).
+// What bounds it: large products the cycles of a step, times a clock that the power
+// limit holds down (8192 x 28672 x 4096 over 8 experts 900 to 930 us, 2.1 PFLOP/s;
+// the unscaled library product of the same sizes 738; 8192^3 450 to 500).  A step of
+// the largest tile, 2048 cycles of products a SIMD, takes 3380, so the matrix units
+// are busy in 55% of 1.73 M cycles.  Without the products, the loads or the
+// multiply-adds the kernel takes 1.75, 1.69 and 1.64 M: none of them alone is the
+// bound, but the operands' reads from LDS between two barriers, which all of these
+// keep (a bare loop of a step's products and multiply-adds takes 2080 cycles, with
+// the reads 2840, with the loads too 3030, with one barrier 3200).  The clock is 1.8
+// GHz, without the products 2.3.  14336 inputs, 4096 outputs, 8192 rows over 8
+// experts (535 to 550 us): 590 tiles are three rounds on 256 CUs, where 2.3 would do.
+// Products of few rows: HBM (60 rows over 512 experts, 2048 inputs, 1536 outputs: 39
+// us, 4.6 TB/s out of the cache), and the smallest the chain of table, routes, rows
+// and sum (2 rows over 8 experts: 7.7 us).
 #include "expert_tiles.h"
 #include "fp8_ops.h"
 #include "fp8_shape.h"

@@ -11,31 +11,34 @@ namespace qmoe {
 // wavefronts.
 enum class Fp8Tile { kRows16, kRows32, k32x64s4, k64x128s3, k128x128s2, k256x256s2 };
 
-// By the tiles that an even spread of the rows over the experts makes (the host knows the offsets' sizes
-// only) for 256 CUs, and in the end by the rounds that they take.  Measured in us, inputs out of cache, the
-// call's 11 us of host time included:
-//                                 rows   32x64   64x128   128x128   256x256
-//   E 8, N 4096, K 2048, rows 2     11.7   13.5    14.3     16.5      22.2
-//                        rows 8     16.6   13.5    14.6     16.7      22.2
-//   E 1, N 4096, K 4096, rows 16    12.0   19.4    22.0     25.4      -
-//                        rows 64    -      19.1    22.2     25.4      35.4
-//                        rows 256   -      21.0    22.8     27.4      51.3
-//                        rows 1024  -      67.0    30.6     29.8      52.0
-//                        rows 2048  -      126     54.2     43.8      54.2
-//                        rows 4096  -      241     103      79.0      65.3
-//   E 1, N 4096, K 14336, rows 16   27.5   51.6    61.0     71.4      -
-//   E 1, N 8192, K 8192, rows 256   -      63.6    39.5     47.5      91.9
-//   E 8, N 4096, K 4096, rows 32    -      38.1    36.0     37.4      44.6
-//                        rows 256   -      47.1    36.1     37.7      46.5
-//                        rows 512   -      57.9    47.5     39.7      47.9
-//                        rows 1024  -      86.9    59.5     58.9      55.0
-//                        rows 2048  -      151     83.5     74.4      64.9
-//                        rows 4096  -      273     138      110       111
-//   E 128, N 2048, K 768, rows 512  -      47.7    42.1     46.2      50.1
-//                         rows 4096 -      63.7    46.2     49.3      53.5
-//   E 512, N 1536, K 2048, rows 60  61.3   39.3    36.8     44.2      49.4
-// The rows are of kRows32; where its tiles leave half of the CUs without one, kRows16 takes 13.5 us for 18.8 (E 1, N
-// 4096, K 14336, one row) and 20.1 for 26.3 (16 rows), and the same at K 2048.
+// By the tiles that an even spread of the rows over the experts makes (the host knows the offsets' sizes only)
+// for 256 CUs, and in the end by the rounds that they take.  The kernel's time in each form in us, whichever the
+// rule takes (the starred), inputs out of cache:
+//                                    16x16   16x32   32x64   64x128  128x128  256x256
+//   E 8, N 4096, K 2048, rows 2        9.4     8.3*   11.4    13.0     16.0     21.9
+//                        rows 8       18.9    19.2    13.8    14.0*    18.5     23.1
+//                        rows 1024     215     178    46.6    32.1     32.8*    31.5
+//   E 1, N 4096, K 4096, rows 16       9.8*   11.2    16.6    19.0     26.3     35.8
+//                        rows 64      23.7    20.3    16.9*   22.4     27.6     36.7
+//                        rows 256     84.6    66.5    19.2*   22.2     29.6     50.5
+//                        rows 1024     315     250    60.0    34.9     31.6*    52.1
+//                        rows 2048       -       -     116    62.6     50.4*    63.4
+//                        rows 4096       -       -     224     119     94.4     69.9*
+//   E 1, N 4096, K 14336, rows 1      16.7*   21.8    43.5    52.8     81.7      110
+//                         rows 16     21.8*   29.0    43.6    53.5     82.3      112
+//                         rows 32     36.8    29.4*   43.6    56.4     82.5      112
+//                         rows 64     70.1    55.0    44.1*   71.0     82.7      115
+//   E 1, N 8192, K 8192, rows 256      302     226    61.7    40.8*    54.0     97.4
+//   E 8, N 4096, K 4096, rows 32      34.3    35.1    34.4    34.9*    36.8     44.2
+//                        rows 256     94.9    81.8    40.5    35.4*    37.0     45.7
+//                        rows 512      174     141    54.7    46.0     38.5*    46.9
+//                        rows 1024     336     269    85.4    58.3     59.4*    55.4
+//                        rows 2048       -       -     143    82.5     78.0     68.3*
+//                        rows 4096       -       -     260     135      115*     113
+//   E 8, N 8192, K 1040, rows 8192       -       -     449     199      152      126*
+//   E 128, N 2048, K 768, rows 512     122     114    45.6    41.4*    45.6     50.0
+//                         rows 4096      -       -    60.5    45.2*    47.9     54.0
+//   E 512, N 1536, K 2048, rows 60    62.9    62.4    38.7    38.0*    44.7     49.8
 // A round of 256 x 256 (one a CU) takes about 1.6 times as long as one of 128 x 128 (two a CU), for twice
 // the work.
 inline Fp8Tile fp8_tile(int E, int N, int rows)
