@@ -39,7 +39,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
     }
 }
 
-// One square a workgroup, so that its maximum is one exchange of four words and no value is read again: thread (r, c) of 16 x 16 holds rows 8 r .. 8 r + 7, columns 8 c .. 8 c + 7.
+// One square a workgroup, so that its maximum is one exchange of four words and no value is read again: thread (r, c)
+// of 16 x 16 holds rows 8 r .. 8 r + 7, columns 8 c .. 8 c + 7.
 // Transposed, the codes pass through LDS, so that a column's 128 bytes leave as one line.
 template <int DT, bool TRANSPOSE>
 __global__ __launch_bounds__(kThreads) void quantize_squares_kernel(const void* __restrict__ x, int rows, int K,
@@ -63,7 +64,9 @@ __global__ __launch_bounds__(kThreads) void quantize_squares_kernel(const void* 
             for (int q = 0; q < 8; ++q) v[r][q] = RowType<DT>::value(raw.v[q]);
         } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[r][q] = r0 + r < rows && k0 + q < K ? RowType<DT>::value(p[(int64_t)r * K + q]) : 0.0f;
+            for (int q = 0; q < 8; ++q) {
+                v[r][q] = r0 + r < rows && k0 + q < K ? RowType<DT>::value(p[(int64_t)r * K + q]) : 0.0f;
+            }
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) top = max(top, magnitude_bits(v[r][q]));
@@ -82,7 +85,9 @@ __global__ __launch_bounds__(kThreads) void quantize_squares_kernel(const void* 
             // K is a multiple of 16: eight columns lie inside or outside together
             if (r0 + r < rows && k0 < K) *reinterpret_cast<u32x2*>(codes + (e * rows + r0 + r) * (int64_t)K + k0) = c;
         }
-        if (threadIdx.x == 0) scales[(e * row_blocks + blockIdx.y) * k_blocks + blockIdx.x] = __builtin_bit_cast(float, bits);
+        if (threadIdx.x == 0) {
+            scales[(e * row_blocks + blockIdx.y) * k_blocks + blockIdx.x] = __builtin_bit_cast(float, bits);
+        }
     } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -103,7 +108,9 @@ __global__ __launch_bounds__(kThreads) void quantize_squares_kernel(const void* 
                     *reinterpret_cast<const u32x4*>(staged + column * kPitch + part);
             }
         }
-        if (threadIdx.x == 0) scales[(e * k_blocks + blockIdx.x) * row_blocks + blockIdx.y] = __builtin_bit_cast(float, bits);
+        if (threadIdx.x == 0) {
+            scales[(e * k_blocks + blockIdx.x) * row_blocks + blockIdx.y] = __builtin_bit_cast(float, bits);
+        }
     }
 }
 
@@ -151,7 +158,8 @@ hipError_t launch_fp8_quantize(const void* x, int64_t row_stride, int64_t rows, 
 {
     const int64_t threads = rows * block_count(K) * 16;
     auto go = [&](auto kernel) {
-        launch(kernel, dim3(blocks_for(threads)), dim3(kThreads), s, x, row_stride, threads, block_count(K), K, codes, scales);
+        launch(kernel, dim3(blocks_for(threads)), dim3(kThreads), s, x, row_stride, threads, block_count(K), K, codes,
+               scales);
     };
     if (dtype == kF32) go(quantize_kernel<kF32>);
     else if (dtype == kBF16) go(quantize_kernel<kBF16>);

@@ -98,7 +98,8 @@ struct Span {
 __device__ inline Span uniform_span(const void* base, uint32_t bytes)
 {
     const uint64_t p = (uint64_t)base;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
     return Span{(const uint8_t*)((uint64_t)hi << 32 | lo), (uint32_t)__builtin_amdgcn_readfirstlane(bytes)};
 }
 
@@ -140,7 +141,8 @@ __device__ inline void clear_behind(const Fp8MatmulArgs& a, int end)
 // Stores two neighbouring blocks of 16 x 16 results: lane 16 g + c holds row c, columns 4 g + i of either in
 // register i.  `out` is the first row and column; rows and cols say how many of them exist (WHOLE: all).
 template <int DT, bool WHOLE>
-__device__ inline void store_blocks(uint16_t* out, int N, int rows, int cols, const f32x4& left, const f32x4& right, int lane)
+__device__ inline void store_blocks(uint16_t* out, int N, int rows, int cols, const f32x4& left, const f32x4& right,
+                                    int lane)
 {
     // lane groups trade columns, so that each lane holds eight neighbours (store_sixteen's order)
     u32x4 v;
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     constexpr int LOADS_A = BM / 8 / WAVES, LOADS_W = BN / 8 / WAVES;  // code loads of a wavefront and step: 8 rows each
     constexpr int LOADS = LOADS_A + LOADS_W + 1;                       // and one of scales
     constexpr int FIRST = LOADS_A + LOADS_W / 2 + 1;                   // those that the first half of a step issues
-    constexpr int A_SLOTS = (BM + kSlots - 1) / kSlots;                // wavefronts that load rows' scales; the next the weights'
+    constexpr int A_SLOTS = (BM + kSlots - 1) / kSlots;                // wavefronts that load rows' scales; the next: weights'
     constexpr int N_BLOCKS = (BN + kFp8Block - 1) / kFp8Block;
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && WAVES % 2 == 0, "load split");
     static_assert(A_SLOTS < WAVES && NT % 2 == 0 && NT * 16 <= kFp8Block, "a wavefront's columns share their scale");
@@ -200,7 +202,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     int load_step = 0;
     auto load_chunk = [&](int lane) { return (uint32_t)((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16; };
     uint32_t code_at[LOADS_A];  // byte offset of the lane's chunk at step 0
-    const uint32_t w_row = (wave * 8 + (lane_now() >> 3)) * (uint32_t)K + load_chunk(lane_now());  // rows behind N: out of bounds
+    // rows behind N: out of bounds
+    const uint32_t w_row = (wave * 8 + (lane_now() >> 3)) * (uint32_t)K + load_chunk(lane_now());
     uint32_t scale_at;          // byte offset of the lane's scale at step 0
     Span a_span, w_span, scale_span;
     // The next item, found between two tiles, where registers are free; and in LDS its rows' source rows in a
@@ -263,7 +266,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
         const uint32_t at = (uint32_t)load_step * kStepBytes;
         uint8_t* const to = lds + stage * STAGE;
         if (q == 0) {
-            load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside, to + SCALES + wave * kSlots * 4);
+            load_to_lds<4>(scale_span.from(load_step * 4), WHOLE || load_step < blocks ? scale_at : kMxOutside,
+                           to + SCALES + wave * kSlots * 4);
             return;
         }
         const int lane = lane_now();
@@ -307,7 +311,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
     float sw;
     const uint32_t x_base = wm * MT * 16 * kStepBytes, w_base = (BM + wn * NT * 16) * kStepBytes;
     auto read_operand = [&](uint32_t at) {
-        return operand(*reinterpret_cast<const u32x4*>(lds + at + read_lo), *reinterpret_cast<const u32x4*>(lds + at + read_hi));
+        return operand(*reinterpret_cast<const u32x4*>(lds + at + read_lo),
+                       *reinterpret_cast<const u32x4*>(lds + at + read_hi));
     };
     auto read_scales = [&](int stage) {
         const uint8_t* from = lds + stage * STAGE + SCALES;
@@ -375,7 +380,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             };
             if (active) {
-                auto read_weight = [&](auto i, int from, int n) { w[decltype(i)::value % W_BUFFERS] = read_operand(from * STAGE + w_base + n * 16 * kStepBytes); };
+                auto read_weight = [&](auto i, int from, int n) {
+                    w[decltype(i)::value % W_BUFFERS] = read_operand(from * STAGE + w_base + n * 16 * kStepBytes);
+                };
                 // Loads are spread over the products (all at once they hold up the wavefront: 14336 inputs, 4096
                 // outputs, 8192 rows over 8 experts: 672 -> 557 us).
                 constexpr int MID = NT / 2 - 2, PLACES = (NT - 2 - MID) * MT;
@@ -439,8 +446,11 @@ __global__ __launch_bounds__(64 * WM * WN) void tiled_kernel(Fp8MatmulArgs a)
             for (int i = 0; i < NT; i += 2) {
                 const int n = tile.n0 + (wn * NT + i) * 16;
                 uint16_t* out = (uint16_t*)a.out + (int64_t)(tile.row0 + m0) * a.N + n;
-                if (tile.n - m0 >= 16 && a.N - n >= 32) store_blocks<DT, true>(out, a.N, 16, 32, acc[i][j], acc[i + 1][j], lane);
-                else store_blocks<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j], acc[i + 1][j], lane);
+                if (tile.n - m0 >= 16 && a.N - n >= 32) {
+                    store_blocks<DT, true>(out, a.N, 16, 32, acc[i][j], acc[i + 1][j], lane);
+                } else {
+                    store_blocks<DT, false>(out, a.N, tile.n - m0, a.N - n, acc[i][j], acc[i + 1][j], lane);
+                }
             }
         }
     }
@@ -482,7 +492,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
         const Span x_span{a.a_codes + a0 * K, (uint32_t)(a_rows * K)}, w_span{a.w_codes + w0 * K, (uint32_t)(w_rows * K)};
         const Span sx_span{(const uint8_t*)(a.a_scales + a0 * blocks), (uint32_t)(a_rows * blocks * 4)};
         const float* const sw_row = a.w_scales + ((int64_t)t.expert * n_blocks + t.n0 / kFp8Block) * blocks;
-        const uint32_t x_at = source < 0 ? kMxOutside : source * (uint32_t)K, sx_at = source < 0 ? kMxOutside : source * (uint32_t)blocks * 4;
+        const uint32_t x_at = source < 0 ? kMxOutside : source * (uint32_t)K;
+        const uint32_t sx_at = source < 0 ? kMxOutside : source * (uint32_t)blocks * 4;
         const uint32_t w_at = c * (uint32_t)K;  // rows behind N: out of bounds
         f32x4 acc[NT] = {};
         for (int b0 = wave; b0 < blocks; b0 += kRowsWaves * kRowsAhead) {
@@ -501,10 +512,12 @@ __global__ __launch_bounds__(64 * kRowsWaves) void rows_kernel(Fp8MatmulArgs a)
                     x[q][h] = __builtin_amdgcn_raw_buffer_load_b128(xr, in && source >= 0 ? x_at + k : kMxOutside, 0, 0);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        w[q][n][h] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? w_at + (uint32_t)(n * 16) * K + k : kMxOutside, 0, 0);
+                        w[q][n][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                            wr, in ? w_at + (uint32_t)(n * 16) * K + k : kMxOutside, 0, 0);
                     }
                 }
-                sx[q] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sx_span.from(there ? b * 4 : 0), there ? sx_at : kMxOutside, 0, 0));
+                sx[q] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                      sx_span.from(there ? b * 4 : 0), there ? sx_at : kMxOutside, 0, 0));
                 sw[q] = there ? sw_row[b] : 0.0f;
             }
 #pragma unroll
@@ -555,8 +568,11 @@ hipError_t launch_tiled(const Fp8MatmulArgs& a, int wgs_per_cu, hipStream_t s)
     int64_t grid = (most_items(a, BM, BN) + 7) / 8 * 8;
     if (grid > kMxCUs * wgs_per_cu) grid = kMxCUs * wgs_per_cu;
     const dim3 threads(64 * WM * WN);
-    if (a.K % kFp8Block == 0 && a.K / kFp8Block >= STAGES) launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), threads, s, a);
-    else launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), threads, s, a);
+    if (a.K % kFp8Block == 0 && a.K / kFp8Block >= STAGES) {
+        launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, true>, dim3((unsigned)grid), threads, s, a);
+    } else {
+        launch(tiled_kernel<DT, MT, NT, WM, WN, STAGES, false>, dim3((unsigned)grid), threads, s, a);
+    }
     return hipGetLastError();
 }
 

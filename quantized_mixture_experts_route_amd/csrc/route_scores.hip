@@ -205,7 +205,8 @@ __device__ inline bool choose_fast(const RouteScoresArgs& a, const typename RowT
         if (lanes > 4) best = merge_dpp<kDppHalfMirror>(best);
         if (lanes > 8) best = merge_dpp<kDppMirror>(best);
         for (int d = 16; d < lanes; d <<= 1) {
-            best = merge(best, Two32{(uint32_t)__shfl_xor((int)best.first, d, kWave), (uint32_t)__shfl_xor((int)best.second, d, kWave)});
+            best = merge(best, Two32{(uint32_t)__shfl_xor((int)best.first, d, kWave),
+                                     (uint32_t)__shfl_xor((int)best.second, d, kWave)});
         }
         float rank = best.first ? value32<EPL>(best.first) : -INFINITY, size_of = best.first ? fabsf(rank) : 0.0f;
         if (a.group_top == 2 && best.second) {
@@ -219,7 +220,8 @@ __device__ inline bool choose_fast(const RouteScoresArgs& a, const typename RowT
         int before = 0;  // groups ahead of the lane's; equal ones are kept or dropped together
         for (int g = 0; g < a.n_groups; ++g) before += readlane_f32(rank, g * lanes) > rank;
         const bool in = mine < a.n_groups, kept = before < a.top_groups;
-        const float least = -wave_largest(in && kept ? -rank : -INFINITY), most = wave_largest(in && !kept ? rank : -INFINITY);
+        const float least = -wave_largest(in && kept ? -rank : -INFINITY);
+        const float most = wave_largest(in && !kept ? rank : -INFINITY);
         // A rank's error goes with what it is the sum of, which with a bias may be far larger than the rank; without
         // one, a score's relative error also has the rounding of l - m, up to 64 u.  Without an expert left in the
         // best of the others nothing hangs on it.
@@ -302,7 +304,9 @@ __device__ inline int choose_exactly(const RouteScoresArgs& a, int lane, const f
             for (int j = 1; j < EPL; ++j) best = merge(best, Two{key[j], 0});
             if (lanes > 1) best = merge(best, Two{dpp_u64<kDppXor1>(best.first), dpp_u64<kDppXor1>(best.second)});
             if (lanes > 2) best = merge(best, Two{dpp_u64<kDppXor2>(best.first), dpp_u64<kDppXor2>(best.second)});
-            if (lanes > 4) best = merge(best, Two{dpp_u64<kDppHalfMirror>(best.first), dpp_u64<kDppHalfMirror>(best.second)});
+            if (lanes > 4) {
+                best = merge(best, Two{dpp_u64<kDppHalfMirror>(best.first), dpp_u64<kDppHalfMirror>(best.second)});
+            }
             if (lanes > 8) best = merge(best, Two{dpp_u64<kDppMirror>(best.first), dpp_u64<kDppMirror>(best.second)});
             for (int d = 16; d < lanes; d <<= 1) {
                 best = merge(best, Two{(uint64_t)__shfl_xor((unsigned long long)best.first, d, kWave),
